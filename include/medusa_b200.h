@@ -484,6 +484,172 @@ medusa_status_t medusa_generate_greedy(const medusa_tree_t* tree, const medusa_d
                                        cudaStream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* A paged cache: rotary positions, attention, compaction                    */
+/* ------------------------------------------------------------------------ */
+
+/* The K/V cache of B sequences in pages that any sequence may own.  Row r of
+ * sequence b lives in page page_table[b, r / page] at row r % page; seq_lens[b]
+ * rows are cached (the prefix).  Pages hold Hkv key/value heads; a query with
+ * H = g Hkv heads shares key head e / g among the g query heads of a group.
+ *   k_pages, v_pages [layers, n_pages, Hkv, page, hd] device, 16-byte aligned
+ *   page_table [B, max_pages] int32 device; only the entries of pages that
+ *              hold rows of the sequence (new tokens included) are read
+ *   seq_lens   [B] int32 device
+ * dtype MEDUSA_F32 or MEDUSA_BF16; page a power of two in [8, 256]; hd a
+ * multiple of 8 in [8, 256]; 1 <= B <= MEDUSA_MAX_B.  Rows of a page past the
+ * sequence's last row may hold anything.  A page that several sequences share
+ * (a common prefix) may be read by all of them; the rows that a call writes
+ * must belong to one sequence.  The struct holds pointers only; the calls do
+ * not keep it.  The pages of the sources have no counterpart ("Medusa API
+ * 参考", tree_decoding names past_key_values without a layout). */
+typedef struct medusa_paged_kv {
+  medusa_dtype_t dtype;
+  int layers, n_pages, Hkv, page, hd;
+  void* k_pages;
+  void* v_pages;
+  int B, max_pages;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+} medusa_paged_kv_t;
+
+/* New tokens of the B sequences are N packed rows: sequence b's chunk is rows
+ * chunk_starts[b] .. chunk_starts[b+1]-1 (chunk_starts [B+1] int32 device,
+ * ascending from 0, last entry <= N; rows behind it are left as they were),
+ * or, with chunk_starts NULL, N / B rows each (N a multiple of B).  Token i of
+ * sequence b is cache row seq_lens[b] + i.  A chunk may be empty.  A chunk
+ * outside [0, N), a negative length, or seq_lens[b] + chunk > max_pages * page
+ * sets MEDUSA_ERR_DEVICE_CHECK and leaves that sequence's rows unwritten, as
+ * does a page id outside [0, n_pages) for the rows in that page (where
+ * attention reads such a page, its keys and values count as zeros). */
+
+typedef enum medusa_rope_layout {
+  MEDUSA_ROPE_HALF = 0,          /* pair i of the rotated part: dimensions i and i + rot/2 */
+  MEDUSA_ROPE_INTERLEAVED = 1    /* dimensions 2i and 2i + 1 */
+} medusa_rope_layout_t;
+
+typedef enum medusa_rope_scaling {
+  MEDUSA_ROPE_NONE = 0,    /* f_i = base^(-2i/rot) */
+  MEDUSA_ROPE_LINEAR = 1,  /* f_i / factor: positions interpolated */
+  MEDUSA_ROPE_NTK = 2,     /* base * factor^(rot/(rot-2)): the slowest pair is interpolated by factor, the fastest kept */
+  MEDUSA_ROPE_YARN = 3     /* pairs that turn more than beta_fast times over original_length positions kept, those
+                            * below beta_slow turns divided by factor, a linear ramp over the pair index between;
+                            * amplitude 0.1 ln(factor) + 1 */
+} medusa_rope_scaling_t;
+
+/* Host.  The rotary frequencies of a head whose first rot dimensions are
+ * rotated: turns[i] (rot/2 entries) is pair i's rotation per position as a
+ * fraction of a turn times 2^64, so that position * turns[i] modulo 2^64 is
+ * the angle at any position without rounding.  *amplitude multiplies cos and
+ * sin.  rot even, 2 <= rot <= 256 (NTK: rot >= 4); base > 1; factor >= 1;
+ * YARN: original_length >= 1, beta_fast > beta_slow > 0 (ignored otherwise). */
+medusa_status_t medusa_rotary_turns(int rot, double base, medusa_rope_scaling_t scaling, double factor,
+                                    int original_length, double beta_fast, double beta_slow,
+                                    uint64_t* turns, float* amplitude);
+
+typedef struct medusa_rotary {
+  medusa_rope_layout_t layout;
+  int rot;                       /* rotated dimensions of a head, even, <= hd; the rest pass through */
+  const uint64_t* turns;         /* [rot / 2] DEVICE copy of medusa_rotary_turns' table */
+  float amplitude;
+} medusa_rotary_t;
+
+/* Rotates the new tokens' queries and keys and writes keys and values into
+ * layer `layer` of the cache, at rows seq_lens[b] + i:
+ *   q [N, H, hd], k, v [N, Hkv, hd] in the cache's dtype, consecutive tokens
+ *              q_stride / k_stride / v_stride elements apart (heads dense; a
+ *              multiple of 16 bytes), so the three may be slices of one fused
+ *              product's output
+ *   q_out [N, H, hd] contiguous; may be q itself when q is contiguous
+ *   positions [N] int32 device: the rotation's position of every token (the
+ *              tree's position_ids), or NULL: the token's cache row
+ * (x, y) -> amplitude (x cos - y sin, y cos + x sin) in fp32, rounded once to
+ * the dtype; v is copied.  seq_lens is not advanced. */
+medusa_status_t medusa_rope_append(const medusa_paged_kv_t* kv, int layer, int N, int H, const void* q,
+                                   int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                   int64_t v_stride, void* q_out, const medusa_rotary_t* rotary,
+                                   const int32_t* positions, const int32_t* chunk_starts, cudaStream_t stream);
+
+/* Bytes for medusa_paged_attention with N query rows of H heads (0 on bad
+ * arguments).  Zero-filled before its first use; two calls that may run at
+ * the same time (two streams, two captured graphs) need one each. */
+size_t medusa_paged_attention_workspace_size(const medusa_paged_kv_t* kv, int N, int H);
+
+/* Attention of the new tokens over layer `layer` of the paged cache, their
+ * own keys and values already in it (medusa_rope_append):
+ *   out[n, e] = sum_j softmax_j(scale q[n, e] . K[j, e / g]) V[j, e / g]
+ * for token n = token i of sequence b (L = seq_lens[b]) over the rows
+ *   tree NULL   j <= L + i: a chunk of a prompt, or one token (decoding)
+ *   tree given  j < L, and L + t for t = i and its ancestors: N = B * T rows,
+ *               chunk_starts must be NULL
+ *   q, out [N, H, hd] contiguous in the cache's dtype, H a multiple of Hkv.
+ * fp32 scores, softmax and accumulation; in bf16 the probabilities enter the
+ * second product rounded to bf16 and the output is rounded once.  scale must
+ * be finite.  Results do not depend on the order in which the GPU runs the
+ * blocks.  A non-finite value row of a NEW token can reach the other new rows
+ * of its sequence (its weight there is zero, and 0 * inf is NaN). */
+medusa_status_t medusa_paged_attention(const medusa_paged_kv_t* kv, int layer, int N, int H, const void* q,
+                                       float scale, const medusa_tree_t* tree, const int32_t* chunk_starts,
+                                       void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes for medusa_paged_accept_kv. */
+size_t medusa_paged_accept_workspace_size(const medusa_paged_kv_t* kv);
+
+/* medusa_accept_kv inside the pages: for every layer and head, with L =
+ * seq_lens[b], a = accept_len[b], n_j = retrieve[best_path[b], j],
+ *   row L+j  <-  row L+n_j,  j = 0..a   (K and V; read before any write),
+ * then new_lens[b] = L + a + 1.  new_lens [B] may be kv->seq_lens itself (the
+ * lengths advance once every row has moved) or another buffer.  An invalid
+ * path, length or page id sets MEDUSA_ERR_DEVICE_CHECK and leaves that
+ * sequence's rows and new_lens[b] as they were. */
+medusa_status_t medusa_paged_accept_kv(const medusa_tree_t* tree, const medusa_paged_kv_t* kv,
+                                       const int32_t* best_path, const int32_t* accept_len, int32_t* new_lens,
+                                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Penalties, biases and grammar masks on the base logits                    */
+/* ------------------------------------------------------------------------ */
+
+#define MEDUSA_MAX_BIAS 1024 /* biased tokens per sequence */
+
+/* What a request asks of its logits, per sequence; every pointer is device
+ * memory and may be NULL (then that part is left out). */
+typedef struct medusa_logit_rules {
+  const int32_t* history;       /* [B, history_cap] tokens so far: the prompt, then what was generated */
+  int history_cap;
+  const int32_t* history_lens;  /* [B], required with history */
+  const int32_t* prompt_lens;   /* [B] leading tokens that are the prompt, NULL: none */
+  const float* repetition;      /* [B] divisor (> 0) of positive, factor of other logits of tokens that occurred */
+  const float* presence;        /* [B] subtracted once from tokens that were generated */
+  const float* frequency;       /* [B] subtracted per occurrence among the generated tokens */
+  const int32_t* bias_ids;      /* [B, n_bias], ids outside [0, V) skipped; a repeated id's values add up */
+  const float* bias;            /* [B, n_bias] */
+  int n_bias;                   /* <= MEDUSA_MAX_BIAS */
+  const uint32_t* allowed;      /* [B, T, ceil(V / 32)] bit v % 32 of word v / 32: token v may follow */
+} medusa_logit_rules_t;
+
+/* The base logits that medusa_evaluate_posterior reads, adjusted per request
+ * and per tree node, in this order, for node i of sequence b and token v:
+ *   z = logits[b,i,v]
+ *   z = z > 0 ? z / repetition : z * repetition  where v occurs in history[b]
+ *       or in tree_tokens on the path from the root to node i (i included)
+ *   z = z - (frequency * c + presence * [c > 0]), c the occurrences of v in
+ *       history past the prompt and on that path
+ *   z = z + the sum of bias over the entries with bias_ids = v (in list order)
+ *   z = -inf where allowed has v's bit clear (a node whose mask is empty gets
+ *       a row of -inf)
+ * A tree of the root alone (T = 1) is the form for single tokens.  Tokens
+ * outside [0, V) are skipped (padding).  history_lens[b] outside [0,
+ * history_cap] or prompt_lens[b] < 0 sets MEDUSA_ERR_DEVICE_CHECK and leaves
+ * that sequence's rows unwritten.
+ *   logits, out [B, T, V] fp32; out may be logits.
+ *   tree_tokens [B, T] int32, required with any of the three penalties.
+ * No workspace.  ["Medusa API参考", evaluate_posterior: the logits it samples
+ * from; the pages name no logit processing.] */
+medusa_status_t medusa_adjust_logits(const medusa_tree_t* tree, int B, int V, const float* logits,
+                                     const int32_t* tree_tokens, const medusa_logit_rules_t* rules, float* out,
+                                     cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* The whole step                                                            */
 /* ------------------------------------------------------------------------ */
 

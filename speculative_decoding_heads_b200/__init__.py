@@ -43,7 +43,13 @@ MEDUSA_BF16 = 1
 MEDUSA_GREEDY = 0
 MEDUSA_TYPICAL = 1
 MEDUSA_NUCLEUS = 2
-MAX_T, MAX_K, MAX_TOPK, MAX_B, MAX_SHARDS = 256, 16, 32, 64, 64
+MEDUSA_ROPE_HALF = 0
+MEDUSA_ROPE_INTERLEAVED = 1
+MEDUSA_ROPE_NONE = 0
+MEDUSA_ROPE_LINEAR = 1
+MEDUSA_ROPE_NTK = 2
+MEDUSA_ROPE_YARN = 3
+MAX_T, MAX_K, MAX_TOPK, MAX_B, MAX_SHARDS, MAX_BIAS = 256, 16, 32, 64, 64, 1024
 
 # Every symbol the header declares (checked by the CPU tests).
 EXPORTED = [
@@ -57,6 +63,9 @@ EXPORTED = [
     "medusa_posterior_workspace_size", "medusa_evaluate_posterior",
     "medusa_accept_kv",
     "medusa_decoder_pack_rows", "medusa_tree_decode_workspace_size", "medusa_tree_decode",
+    "medusa_rotary_turns", "medusa_rope_append",
+    "medusa_paged_attention_workspace_size", "medusa_paged_attention",
+    "medusa_paged_accept_workspace_size", "medusa_paged_accept_kv", "medusa_adjust_logits",
     "medusa_step_workspace_size", "medusa_step", "medusa_step_host",
     "medusa_generate_workspace_size", "medusa_generate_greedy", "medusa_generate",
 ]
@@ -112,6 +121,25 @@ class DecoderModel(ctypes.Structure):
                 ("layer", ctypes.POINTER(DecoderLayer)), ("final_norm", _vp), ("lm_head", _vp)]
 
 
+class PagedKVArgs(ctypes.Structure):
+    """Mirror of ``medusa_paged_kv_t``."""
+    _fields_ = [("dtype", _i32), ("layers", _i32), ("n_pages", _i32), ("Hkv", _i32), ("page", _i32), ("hd", _i32),
+                ("k_pages", _vp), ("v_pages", _vp), ("B", _i32), ("max_pages", _i32), ("page_table", _vp),
+                ("seq_lens", _vp)]
+
+
+class RotaryArgs(ctypes.Structure):
+    """Mirror of ``medusa_rotary_t``."""
+    _fields_ = [("layout", _i32), ("rot", _i32), ("turns", _vp), ("amplitude", _f32)]
+
+
+class LogitRules(ctypes.Structure):
+    """Mirror of ``medusa_logit_rules_t``."""
+    _fields_ = [("history", _vp), ("history_cap", _i32), ("history_lens", _vp), ("prompt_lens", _vp),
+                ("repetition", _vp), ("presence", _vp), ("frequency", _vp), ("bias_ids", _vp), ("bias", _vp),
+                ("n_bias", _i32), ("allowed", _vp)]
+
+
 def _sig(name, restype, argtypes):
     fn = getattr(_lib, name)
     fn.restype = restype
@@ -154,6 +182,17 @@ _sig("medusa_generate_greedy", _i32, [_vp, ctypes.POINTER(DecoderModel), _vp, _v
 _sig("medusa_generate", _i32, [_vp, ctypes.POINTER(DecoderModel), _vp, _vp, _vp, _i32, _f32, _f32, _f32, _f32,
                                ctypes.POINTER(ctypes.c_float), _pi32, _i32, _i32, _vp, _vp, _i32, _pi32, _pi32, _i32,
                                _pi32, _vp, _sz, _vp])
+_i64 = ctypes.c_int64
+_pkv = ctypes.POINTER(PagedKVArgs)
+_sig("medusa_rotary_turns", _i32, [_i32, ctypes.c_double, _i32, ctypes.c_double, _i32, ctypes.c_double, ctypes.c_double,
+                                   _pu64, ctypes.POINTER(_f32)])
+_sig("medusa_rope_append", _i32, [_pkv, _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                  ctypes.POINTER(RotaryArgs), _vp, _vp, _vp])
+_sig("medusa_paged_attention_workspace_size", _sz, [_pkv, _i32, _i32])
+_sig("medusa_paged_attention", _i32, [_pkv, _i32, _i32, _i32, _vp, _f32, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("medusa_paged_accept_workspace_size", _sz, [_pkv])
+_sig("medusa_paged_accept_kv", _i32, [_vp, _pkv, _vp, _vp, _vp, _vp, _sz, _vp])
+_sig("medusa_adjust_logits", _i32, [_vp, _i32, _i32, _vp, _vp, ctypes.POINTER(LogitRules), _vp, _vp])
 _sig("medusa_step_workspace_size", _sz, [ctypes.POINTER(StepArgs)])
 _sig("medusa_step", _i32, [ctypes.POINTER(StepArgs), _vp, _sz, _vp])
 _sig("medusa_step_host", _i32, [ctypes.POINTER(StepArgs), ctypes.POINTER(StepHostIO), _vp, _sz, _vp])
@@ -626,6 +665,182 @@ def medusa_generate(tree: Tree, model: Decoder, W1, b1, Wout, prompt, n_new: int
                               ctypes.byref(n), _p(ws), nbytes, _stream(stream))
     _check(st)
     return list(out), list(acc[:n.value])
+
+
+# ---------------------------------------------------------------------------
+# a paged cache, and the requests' logits
+# ---------------------------------------------------------------------------
+
+
+class PagedKV:
+    """The paged K/V cache of B sequences (``medusa_paged_kv_t``): k_pages, v_pages [layers, n_pages,
+    Hkv, page, hd] (bf16 or fp32), page_table [B, max_pages] int32, seq_lens [B] int32.  Row r of
+    sequence b is row r % page of page page_table[b, r // page].  The object keeps the tensors and
+    checks them once; their contents may change between calls."""
+
+    def __init__(self, k_pages, v_pages, page_table, seq_lens):
+        _require(isinstance(k_pages, torch.Tensor) and k_pages.dim() == 5, "k_pages must be [layers, n_pages, Hkv, page, hd]")
+        _require(isinstance(page_table, torch.Tensor) and page_table.dim() == 2, "page_table must be [B, max_pages]")
+        dtype = _dtype(k_pages)
+        _spec("k_pages", k_pages, k_pages.shape, k_pages.dtype)
+        _spec("v_pages", v_pages, k_pages.shape, k_pages.dtype)
+        _spec("page_table", page_table, page_table.shape, torch.int32)
+        B = page_table.shape[0]
+        _spec("seq_lens", seq_lens, (B,), torch.int32)
+        self.k_pages, self.v_pages, self.page_table, self.seq_lens = k_pages, v_pages, page_table, seq_lens
+        self.dtype, self.B = k_pages.dtype, B
+        self.layers, self.n_pages, self.Hkv, self.page, self.hd = k_pages.shape
+        _require(len({t.device for t in (k_pages, v_pages, page_table, seq_lens)}) == 1,
+                 "the pages, the page table and the lengths must be on one device")
+        self.c = PagedKVArgs(dtype, *k_pages.shape, k_pages.data_ptr(), v_pages.data_ptr(), B, page_table.shape[1],
+                             page_table.data_ptr(), seq_lens.data_ptr())
+
+
+class Rotary:
+    """Rotary frequencies on the current device (``medusa_rotary_turns``): the first ``rot``
+    dimensions of a head are rotated, in ``layout``, with ``scaling`` for long contexts."""
+
+    def __init__(self, rot: int, layout: int = MEDUSA_ROPE_HALF, base: float = 10000.0, scaling: int = MEDUSA_ROPE_NONE,
+                 factor: float = 1.0, original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
+        turns, amplitude = medusa_rotary_turns(rot, base, scaling, factor, original_length, beta_fast, beta_slow)
+        self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64, device="cuda")
+        self.layout, self.rot, self.amplitude = int(layout), int(rot), amplitude
+        self.c = RotaryArgs(self.layout, self.rot, _p(self.turns).value, amplitude)
+
+
+def medusa_rotary_turns(rot: int, base: float = 10000.0, scaling: int = MEDUSA_ROPE_NONE, factor: float = 1.0,
+                        original_length: int = 4096, beta_fast: float = 32.0, beta_slow: float = 1.0):
+    """(rot/2 rotations per position in turns times 2^64, the amplitude of cos and sin), as the C call documents."""
+    turns = (ctypes.c_uint64 * max(1, int(rot) // 2))()
+    amplitude = _f32(0.0)
+    _check(_lib.medusa_rotary_turns(int(rot), float(base), int(scaling), float(factor), int(original_length),
+                                    float(beta_fast), float(beta_slow), turns, ctypes.byref(amplitude)))
+    return list(turns), amplitude.value
+
+
+def _token_rows(name: str, t, heads: int, hd: int, dtype):
+    """(token stride in elements) of a [N, heads, hd] tensor whose heads are dense."""
+    _require(isinstance(t, torch.Tensor) and t.dim() == 3 and t.shape[1:] == (heads, hd),
+             f"{name} must be [N, {heads}, {hd}]")
+    _require(t.dtype == dtype, f"{name} has dtype {t.dtype}, expected {dtype}")
+    _require((t.stride(2) == 1 or hd == 1) and (t.stride(1) == hd or heads == 1),
+             f"the heads of a token of {name} must be dense")
+    return t.stride(0) if t.shape[0] > 1 else heads * hd
+
+
+def _chunk_starts(kv: PagedKV, N: int, chunk_starts):
+    _require(N >= 1, "at least one token")
+    if chunk_starts is None:
+        _require(N % kv.B == 0, "without chunk_starts every sequence has N / B tokens")
+    else:
+        _spec("chunk_starts", chunk_starts, (kv.B + 1,), torch.int32)
+
+
+def medusa_rope_append(kv: PagedKV, layer: int, q, k, v, q_out, rotary: Rotary, positions=None, chunk_starts=None,
+                       stream=None):
+    """Rotates q [N, H, hd] into q_out and k [N, Hkv, hd] into layer ``layer`` of the cache, with v
+    next to it, at rows seq_lens[b] + i.  q, k and v may be slices of one fused product's output
+    (any token stride of whole 16-byte units).  positions [N] int32: the rotation's positions, else
+    the cache rows; chunk_starts [B+1] int32: ragged chunks, else N / B tokens each."""
+    _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be [N, H, hd]")
+    N, H, _ = q.shape
+    qs = _token_rows("q", q, H, kv.hd, kv.dtype)
+    ks = _token_rows("k", k, kv.Hkv, kv.hd, kv.dtype)
+    vs = _token_rows("v", v, kv.Hkv, kv.hd, kv.dtype)
+    _require(k.shape[0] == N and v.shape[0] == N, "q, k and v must hold the same tokens")
+    _spec("q_out", q_out, (N, H, kv.hd), kv.dtype)
+    _chunk_starts(kv, N, chunk_starts)
+    if positions is not None:
+        _spec("positions", positions, (N,), torch.int32)
+    _p(kv.k_pages)
+    _p(rotary.turns)
+    _check(_lib.medusa_rope_append(ctypes.byref(kv.c), int(layer), N, H, _p(q), qs, _p(k), ks, _p(v), vs, _p(q_out),
+                                   ctypes.byref(rotary.c), _p(positions), _p(chunk_starts), _stream(stream)))
+
+
+def medusa_paged_attention_workspace_size(kv: PagedKV, N: int, H: int) -> int:
+    return int(_lib.medusa_paged_attention_workspace_size(ctypes.byref(kv.c), int(N), int(H)))
+
+
+def medusa_paged_attention(kv: PagedKV, layer: int, q, out, scale: float, ws, tree: Optional[Tree] = None,
+                           chunk_starts=None, stream=None):
+    """Attention of q [N, H, hd] (the packed new tokens) over layer ``layer`` of the cache, which
+    already holds their keys and values, into out [N, H, hd].  Without a tree token i of a sequence
+    sees the prefix and the chunk's tokens up to itself; with one, the prefix, its ancestors and
+    itself (N = B * tree.T)."""
+    _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be [N, H, hd]")
+    N, H, _ = q.shape
+    _spec("q", q, (N, H, kv.hd), kv.dtype)
+    _spec("out", out, (N, H, kv.hd), kv.dtype)
+    _chunk_starts(kv, N, chunk_starts)
+    if tree is not None:
+        _require(N == kv.B * tree.T and chunk_starts is None,
+                 f"with a tree q must hold {tree.T} rows per sequence, and chunk_starts be absent")
+    nbytes = _nbytes("ws", ws)
+    _p(kv.k_pages)
+    _check(_lib.medusa_paged_attention(ctypes.byref(kv.c), int(layer), N, H, _p(q), float(scale),
+                                       None if tree is None else tree.handle, _p(chunk_starts), _p(out), _p(ws), nbytes,
+                                       _stream(stream)))
+
+
+def medusa_paged_accept_workspace_size(kv: PagedKV) -> int:
+    return int(_lib.medusa_paged_accept_workspace_size(ctypes.byref(kv.c)))
+
+
+def medusa_paged_accept_kv(tree: Tree, kv: PagedKV, best_path, accept_len, new_lens, ws, stream=None):
+    """S7 inside the pages, every layer: the accepted rows move to the end of the prefix, and
+    new_lens [B] (kv.seq_lens itself, or another buffer) receives the new lengths."""
+    for name, t in (("best_path", best_path), ("accept_len", accept_len), ("new_lens", new_lens)):
+        _spec(name, t, (kv.B,), torch.int32)
+    nbytes = _nbytes("ws", ws)
+    _p(kv.k_pages)
+    _check(_lib.medusa_paged_accept_kv(tree.handle, ctypes.byref(kv.c), _p(best_path), _p(accept_len), _p(new_lens),
+                                       _p(ws), nbytes, _stream(stream)))
+
+
+def medusa_adjust_logits(tree: Tree, logits, tree_tokens, out, history=None, history_lens=None, prompt_lens=None,
+                         repetition=None, presence=None, frequency=None, bias_ids=None, bias=None, allowed=None,
+                         stream=None):
+    """Penalties, biases and a grammar mask on the base logits [B, T, V] of every tree node, into out
+    (which may be logits).  history [B, cap] int32 with history_lens and prompt_lens [B] (its leading
+    prompt tokens count for the repetition penalty only); repetition, presence, frequency [B] fp32;
+    bias_ids / bias [B, n]; allowed [B, T, ceil(V / 32)] int32, a bit per token."""
+    _require(isinstance(logits, torch.Tensor) and logits.dim() == 3, "logits must be [B, T, V]")
+    B, T, V = logits.shape
+    _require(T == tree.T, f"logits hold {T} tree nodes per sequence; the tree has {tree.T}")
+    _spec("logits", logits, (B, T, V), torch.float32)
+    _spec("out", out, (B, T, V), torch.float32)
+    r = LogitRules()
+    penalties = [("repetition", repetition), ("presence", presence), ("frequency", frequency)]
+    if tree_tokens is not None or any(t is not None for _, t in penalties):
+        _spec("tree_tokens", tree_tokens, (B, T), torch.int32)
+    for name, t in penalties:
+        if t is not None:
+            _spec(name, t, (B,), torch.float32)
+    if history is not None:
+        _require(isinstance(history, torch.Tensor) and history.dim() == 2 and history.shape[1] >= 1,
+                 "history must be [B, cap]")
+        _spec("history", history, (B, history.shape[1]), torch.int32)
+        _spec("history_lens", history_lens, (B,), torch.int32)
+        r.history_cap = history.shape[1]
+    else:
+        _require(history_lens is None and prompt_lens is None, "history_lens and prompt_lens need a history")
+    if prompt_lens is not None:
+        _spec("prompt_lens", prompt_lens, (B,), torch.int32)
+    _require((bias_ids is None) == (bias is None), "bias_ids and bias go together")
+    if bias is not None:
+        _require(isinstance(bias_ids, torch.Tensor) and bias_ids.dim() == 2 and 1 <= bias_ids.shape[1] <= MAX_BIAS,
+                 f"bias_ids must be [B, n] with 1 <= n <= {MAX_BIAS}")
+        _spec("bias_ids", bias_ids, (B, bias_ids.shape[1]), torch.int32)
+        _spec("bias", bias, bias_ids.shape, torch.float32)
+        r.n_bias = bias_ids.shape[1]
+    if allowed is not None:
+        _spec("allowed", allowed, (B, T, (V + 31) // 32), torch.int32)
+    for name, t in [("history", history), ("history_lens", history_lens), ("prompt_lens", prompt_lens),
+                    ("bias_ids", bias_ids), ("bias", bias), ("allowed", allowed)] + penalties:
+        setattr(r, name, _p(t))
+    _check(_lib.medusa_adjust_logits(tree.handle, B, V, _p(logits), _p(tree_tokens), ctypes.byref(r), _p(out),
+                                     _stream(stream)))
 
 
 def make_step_args(tree: Tree, t: dict, mode: int, temperature=0.0, eps=0.09, alpha=0.3,

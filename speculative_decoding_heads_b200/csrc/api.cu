@@ -84,7 +84,7 @@ medusa_status_t device_status_read(int32_t* status, int32_t* detail, int clear) 
 }
 
 // Checks shared by the calls that take a tree.
-static medusa_status_t check_tree(const medusa_tree_t* tree, const char* fn) {
+medusa_status_t check_tree(const medusa_tree_t* tree, const char* fn) {
   if (!tree) return fail(MEDUSA_ERR_INVALID_ARG, std::string(fn) + ": tree is null");
   if (!tree->dev_block) return fail(MEDUSA_ERR_INVALID_ARG, std::string(fn) + ": tree was created without upload");
   const int dev = current_device();

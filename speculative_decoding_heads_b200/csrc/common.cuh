@@ -21,6 +21,11 @@ enum DeviceDetail : int {
   kDetailDecoderWait = 8,     // tree decode: a matrix product's copy or product never completed
   kDetailDecoderToken = 9,    // tree decode: a tree token outside [0, V)
   kDetailDecoderSeqLen = 10,  // tree decode: seq_lens[b] + T > Lcap
+  kDetailPagedChunk = 11,     // paged calls: a chunk outside the packed rows, or a sequence past its page table
+  kDetailPagedPage = 12,      // paged calls: a page id outside [0, n_pages)
+  kDetailPagedAccept = 13,    // paged_accept_kv: bad path, accept length or sequence length
+  kDetailPagedWait = 14,      // paged attention: a copy or product never completed
+  kDetailLogitHistory = 15,   // adjust_logits: a history length outside its buffer
 };
 
 // Address of the current device's status word ([0] status, [1] detail).

@@ -47,6 +47,9 @@ medusa_status_t device_status_read(int32_t* status, int32_t* detail, int clear);
 // Number of SMs of the current device (cached per device).
 int sm_count();
 
+// A tree that the current device can use (api.cu).
+medusa_status_t check_tree(const medusa_tree_t* tree, const char* fn);
+
 // S4 outputs, when the heads kernel also builds the candidate tree (medusa_step).
 struct TreeBuild {
   TreeDev t;
@@ -154,6 +157,29 @@ uint16_t* decoder_final_rows(void* ws, int ntok, int D, int F, int V);
 medusa_status_t launch_tree_decode(const TreeDev& t, const medusa_decoder_t* m, int B, const int32_t* tree_tokens,
                                    void* k_cache, void* v_cache, int Lcap, const int32_t* seq_lens,
                                    float* logits, float* hidden, void* ws, cudaStream_t stream);
+
+// The paged cache as kernels see it (paged_api.cu builds it from checked arguments).
+struct PagedDev {
+  int n_pages, Hkv, page_shift, hd, B, max_pages;
+  const int32_t* table;    // [B, max_pages]
+  const int32_t* lens;     // [B]
+  void* k;                 // one layer [n_pages, Hkv, page, hd] (accept: all layers)
+  void* v;
+};
+
+medusa_status_t launch_rope_append(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const void* q,
+                                   int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   void* q_out, const medusa_rotary_t& rotary, const int32_t* positions,
+                                   const int32_t* starts, cudaStream_t stream);
+size_t paged_attention_workspace_bytes(const PagedDev& kv, medusa_dtype_t dtype, int N, int H);
+medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const void* q,
+                                       float scale, const TreeDev* tree, const int32_t* starts, void* out, void* ws,
+                                       cudaStream_t stream);
+medusa_status_t launch_paged_accept(const TreeDev& t, const PagedDev& kv, int layers, medusa_dtype_t dtype,
+                                    const int32_t* best_path, const int32_t* accept_len, int32_t* new_lens, void* ws,
+                                    cudaStream_t stream);
+medusa_status_t launch_adjust_logits(const TreeDev& t, int B, int V, const float* logits, const int32_t* tree_tokens,
+                                     const medusa_logit_rules_t& rules, float* out, cudaStream_t stream);
 
 // cuTensorMapEncodeTiled (PFN_cuTensorMapEncodeTiled_v12000), or null.
 void* tensor_map_encoder();

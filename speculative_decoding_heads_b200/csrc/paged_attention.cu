@@ -1,0 +1,334 @@
+// Attention of new tokens over a paged cache, fp32 arithmetic on the CUDA
+// cores: every dtype, head size and group size (the tensor-core kernel of
+// paged_attention_tc.cu takes bf16 heads of 64 and 128).
+//
+// One pass over the keys with a running maximum and sum per query row: with
+// m' = max(m, max_j s_j), O <- O 2^(m - m') + sum_j 2^(s_j - m') V_j and the
+// same for the sum l, the output is O / l whatever the order of the blocks.
+// A CTA holds R query rows and takes 64 keys at a time through shared memory
+// as fp32; a thread owns R / 16 or R / 8 rows x 4 keys of the scores and the
+// same rows x HD / 16 dimensions of O, so one 16-byte shared-memory read
+// feeds 16 products.  R = 16 where the largest chunk fits (decoding and small
+// trees, bound by the cache's bytes), 64 otherwise (bound by fp32 arithmetic).
+#include "paged_work.cuh"
+
+namespace medusa {
+namespace {
+
+using namespace paged;
+
+constexpr int kBK = 64;          // keys per block
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* p);
+template <>
+__device__ __forceinline__ float4 load4<float>(const float* p) { return *reinterpret_cast<const float4*>(p); }
+template <>
+__device__ __forceinline__ float4 load4<uint16_t>(const uint16_t* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(bf16lo(w.x), bf16hi(w.x), bf16lo(w.y), bf16hi(w.y));
+}
+__device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store4(uint16_t* p, float4 v) {
+  *reinterpret_cast<uint2*>(p) =
+      make_uint2(static_cast<uint32_t>(f32_to_bf16_rne(v.x)) | (static_cast<uint32_t>(f32_to_bf16_rne(v.y)) << 16),
+                 static_cast<uint32_t>(f32_to_bf16_rne(v.z)) | (static_cast<uint32_t>(f32_to_bf16_rne(v.w)) << 16));
+}
+
+template <int HD, int R>
+struct Shape {
+  static constexpr int kRows = R == 16 ? 2 : 4;       // query rows per thread
+  static constexpr int kThreads = R / kRows * 16;     // 16 threads side by side per row group
+  static constexpr int kPitch = HD + 4;               // floats per row: conflict-free 16-byte reads down a column
+  static constexpr int kPPitch = kBK + 4;
+  static constexpr size_t kSmem = (static_cast<size_t>(R + 2 * kBK) * kPitch + R * kPPitch) * sizeof(float);
+  static constexpr int kPerSm = kSmem > 110 * 1024 ? 1 : kSmem > 73 * 1024 ? 2 : 3;
+};
+
+template <typename T, int HD, int R>
+__global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(const Work w, const T* q, float scale_log2, T* out) {
+  using S = Shape<HD, R>;
+  using C = Cut<R, kBK>;
+  constexpr int NT = S::kThreads, RR = S::kRows, DV = HD / 64;   // DV groups of 4 dimensions per thread
+  extern __shared__ __align__(16) float sh[];
+  float* qs = sh;
+  float* ks = qs + R * S::kPitch;
+  float* vs = ks + kBK * S::kPitch;
+  float* ps = vs + kBK * S::kPitch;
+  __shared__ Plan plan;
+  __shared__ int s_last;
+  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+  const int hd = w.kv.hd, g = w.g, hd4 = hd / 4;
+  unsigned long long begin, end;
+  int b0 = 0, h0 = 0;
+  C::template plan<NT>(w, plan, &begin, &end, &b0, &h0);
+  if (begin >= end) return;
+  const unsigned long long W = plan.before[w.kv.B];
+  unsigned long long left = end - begin;
+  Piece x = C::first_piece(w, plan, begin, b0, h0, left);
+  const int shift = w.kv.page_shift, mask = (1 << shift) - 1;
+  for (;;) {
+    const int b = x.b, L = plan.L[b], n = plan.n[b], first = plan.first[b];
+    const int rows = min(R, n * g - x.tile * R);
+    const int keys = static_cast<int>(C::keys(w, plan, b, x.tile));
+    __syncthreads();                       // the piece before is done with shared memory
+    for (int i = tid; i < R * (HD / 4); i += NT) {
+      const int r = i / (HD / 4), d = i - r * (HD / 4);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < rows && d < hd4) {
+        const int rr = x.tile * R + r, tok = rr / g, head = x.h * g + rr - tok * g;
+        v = load4<T>(q + (static_cast<size_t>(first + tok) * w.H + head) * hd + 4 * d);
+      }
+      *reinterpret_cast<float4*>(qs + r * S::kPitch + 4 * d) = v;
+    }
+    float m[RR], l[RR], o[RR][DV][4];
+#pragma unroll
+    for (int r = 0; r < RR; ++r) {
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+#pragma unroll
+      for (int d = 0; d < DV; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[r][d][e] = 0.f;
+    }
+    for (int kb = x.kb0; kb < x.kb1; ++kb) {
+      const int j0 = kb * kBK;
+      __syncthreads();
+      for (int i = tid; i < kBK * (HD / 4); i += NT) {
+        const int r = i / (HD / 4), d = i - r * (HD / 4);
+        float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
+        if (j0 + r < keys && d < hd4) {    // rows past the sequence are not read
+          const int page = w.kv.table[static_cast<long long>(b) * w.kv.max_pages + ((j0 + r) >> shift)];
+          if (page >= 0 && page < w.kv.n_pages) {
+            const long long off =
+                (((static_cast<long long>(page) * w.kv.Hkv + x.h) << shift) + ((j0 + r) & mask)) * hd + 4 * d;
+            kk = load4<T>(static_cast<const T*>(w.kv.k) + off);
+            vv = load4<T>(static_cast<const T*>(w.kv.v) + off);
+          } else {
+            set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
+          }
+        }
+        *reinterpret_cast<float4*>(ks + r * S::kPitch + 4 * d) = kk;
+        *reinterpret_cast<float4*>(vs + r * S::kPitch + 4 * d) = vv;
+      }
+      __syncthreads();
+      float s[RR][4];
+#pragma unroll
+      for (int r = 0; r < RR; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[r][c] = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < HD / 4; ++d) {
+        float4 a[RR], k4[4];
+#pragma unroll
+        for (int r = 0; r < RR; ++r) a[r] = *reinterpret_cast<const float4*>(qs + (ty * RR + r) * S::kPitch + 4 * d);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) k4[c] = *reinterpret_cast<const float4*>(ks + (tx + 16 * c) * S::kPitch + 4 * d);
+#pragma unroll
+        for (int r = 0; r < RR; ++r)
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            s[r][c] = fmaf(a[r].x, k4[c].x, fmaf(a[r].y, k4[c].y, fmaf(a[r].z, k4[c].z, fmaf(a[r].w, k4[c].w, s[r][c]))));
+      }
+#pragma unroll
+      for (int r = 0; r < RR; ++r) {
+        const int rr = x.tile * R + ty * RR + r, tok = rr / g;
+        float mx = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = j0 + tx + 16 * c, rel = j - L;
+          bool see;
+          if (w.t.T > 0)
+            see = rel < 0 || (rel < n && tok < n && ((w.t.anc[tok * w.t.W + (rel >> 6)] >> (rel & 63)) & 1ull));
+          else
+            see = rel <= tok && rel < n;
+          s[r][c] = see ? s[r][c] * scale_log2 : -INFINITY;
+          mx = fmaxf(mx, s[r][c]);
+        }
+        for (int off = 8; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const float mn = fmaxf(m[r], mx), ref = mn == -INFINITY ? 0.f : mn;
+        const float f = exp2f(m[r] - ref);
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float p = exp2f(s[r][c] - ref);
+          ps[(ty * RR + r) * S::kPPitch + tx + 16 * c] = p;
+          sum += p;
+        }
+        for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        m[r] = mn;
+        l[r] = l[r] * f + sum;
+#pragma unroll
+        for (int d = 0; d < DV; ++d)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[r][d][e] *= f;
+      }
+      __syncwarp();                        // a row's probabilities are written and read by one half-warp
+#pragma unroll 4
+      for (int j = 0; j < kBK; j += 4) {
+        float4 pr[RR];
+#pragma unroll
+        for (int r = 0; r < RR; ++r) pr[r] = *reinterpret_cast<const float4*>(ps + (ty * RR + r) * S::kPPitch + j);
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+          for (int d = 0; d < DV; ++d) {
+            const float4 v4 = *reinterpret_cast<const float4*>(vs + (j + u) * S::kPitch + 64 * d + 4 * tx);
+#pragma unroll
+            for (int r = 0; r < RR; ++r) {
+              const float p = u == 0 ? pr[r].x : u == 1 ? pr[r].y : u == 2 ? pr[r].z : pr[r].w;
+              o[r][d][0] = fmaf(p, v4.x, o[r][d][0]);
+              o[r][d][1] = fmaf(p, v4.y, o[r][d][1]);
+              o[r][d][2] = fmaf(p, v4.z, o[r][d][2]);
+              o[r][d][3] = fmaf(p, v4.w, o[r][d][3]);
+            }
+          }
+      }
+    }
+    bool write = C::whole(x);
+    if (!write) {
+      // Leave the piece in this CTA's slot; the last piece of the unit joins them.
+      float* slot = w.slots + C::slot(blockIdx.x, x.start, W) * slot_floats(R, HD);
+#pragma unroll
+      for (int r = 0; r < RR; ++r) {
+        const int row = ty * RR + r;
+        if (tx == 0) {
+          __stcg(slot + row, m[r]);
+          __stcg(slot + R + row, l[r]);
+        }
+#pragma unroll
+        for (int d = 0; d < DV; ++d)
+          __stcg(reinterpret_cast<float4*>(slot + 2 * R + row * HD + 64 * d + 4 * tx),
+                 make_float4(o[r][d][0], o[r][d][1], o[r][d][2], o[r][d][3]));
+      }
+      __threadfence();
+      __syncthreads();
+      const int c_lo = C::owner(x.start, W), c_hi = C::owner(x.start + x.blocks - 1, W);
+      if (tid == 0) {
+        unsigned* ctr = w.counters + static_cast<size_t>(plan.tile0[b] + x.tile) * w.kv.Hkv + x.h;
+        s_last = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(c_hi - c_lo);
+        if (s_last) *ctr = 0u;
+      }
+      __syncthreads();
+      write = s_last != 0;
+      if (write) {
+        __threadfence();
+#pragma unroll
+        for (int r = 0; r < RR; ++r) {
+          const int row = ty * RR + r;
+          m[r] = -INFINITY;
+          for (int c = c_lo; c <= c_hi; ++c) m[r] = fmaxf(m[r], __ldcg(w.slots + C::slot(c, x.start, W) * slot_floats(R, HD) + row));
+          l[r] = 0.f;
+#pragma unroll
+          for (int d = 0; d < DV; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[r][d][e] = 0.f;
+          const float ref = m[r] == -INFINITY ? 0.f : m[r];
+          for (int c = c_lo; c <= c_hi; ++c) {
+            const float* sl = w.slots + C::slot(c, x.start, W) * slot_floats(R, HD);
+            const float f = exp2f(__ldcg(sl + row) - ref);
+            l[r] += f * __ldcg(sl + R + row);
+#pragma unroll
+            for (int d = 0; d < DV; ++d) {
+              const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + 2 * R + row * HD + 64 * d + 4 * tx));
+              o[r][d][0] = fmaf(f, v.x, o[r][d][0]);
+              o[r][d][1] = fmaf(f, v.y, o[r][d][1]);
+              o[r][d][2] = fmaf(f, v.z, o[r][d][2]);
+              o[r][d][3] = fmaf(f, v.w, o[r][d][3]);
+            }
+          }
+        }
+      }
+    }
+    if (write) {
+#pragma unroll
+      for (int r = 0; r < RR; ++r) {
+        const int row = ty * RR + r;
+        if (row >= rows) continue;
+        const int rr = x.tile * R + row, tok = rr / g, head = x.h * g + rr - tok * g;
+        const float inv = 1.f / l[r];
+        T* dst = out + (static_cast<size_t>(first + tok) * w.H + head) * hd;
+#pragma unroll
+        for (int d = 0; d < DV; ++d)
+          if (64 * d + 4 * tx < hd)
+            store4(dst + 64 * d + 4 * tx, make_float4(o[r][d][0] * inv, o[r][d][1] * inv, o[r][d][2] * inv, o[r][d][3] * inv));
+      }
+    }
+    if (left == 0) break;
+    C::next_piece(w, plan, x, left);
+  }
+}
+
+struct Choice {
+  int R, HD, per_sm;
+};
+
+// R = 16 while a sequence's rows of one key head fit in 16 on average.
+Choice choose(const PagedDev& kv, int N, int H) {
+  Choice c;
+  c.HD = kv.hd <= 64 ? 64 : kv.hd <= 128 ? 128 : 256;
+  c.R = static_cast<long long>(N) * (H / kv.Hkv) <= 16ll * kv.B ? 16 : 64;
+  auto per = [&](auto hd) {
+    constexpr int kHD = decltype(hd)::value;
+    return c.R == 16 ? Shape<kHD, 16>::kPerSm : Shape<kHD, 64>::kPerSm;
+  };
+  c.per_sm = c.HD == 64 ? per(std::integral_constant<int, 64>{})
+             : c.HD == 128 ? per(std::integral_constant<int, 128>{})
+                           : per(std::integral_constant<int, 256>{});
+  return c;
+}
+
+template <typename T, int HD, int R>
+cudaError_t run(const Work& w, int grid, const void* q, float scale_log2, void* out, cudaStream_t stream) {
+  auto fn = paged_attn_kernel<T, HD, R>;
+  constexpr size_t smem = Shape<HD, R>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  fn<<<grid, Shape<HD, R>::kThreads, smem, stream>>>(w, static_cast<const T*>(q), scale_log2, static_cast<T*>(out));
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t run_for(const Choice& c, const Work& w, int grid, const void* q, float s, void* out, cudaStream_t st) {
+  if (c.R == 16) {
+    if (c.HD == 64) return run<T, 64, 16>(w, grid, q, s, out, st);
+    if (c.HD == 128) return run<T, 128, 16>(w, grid, q, s, out, st);
+    return run<T, 256, 16>(w, grid, q, s, out, st);
+  }
+  if (c.HD == 64) return run<T, 64, 64>(w, grid, q, s, out, st);
+  if (c.HD == 128) return run<T, 128, 64>(w, grid, q, s, out, st);
+  return run<T, 256, 64>(w, grid, q, s, out, st);
+}
+
+}  // namespace
+
+size_t paged_attention_workspace_bytes(const PagedDev& kv, medusa_dtype_t dtype, int N, int H) {
+  (void)dtype;
+  const Choice c = choose(kv, N, H);
+  return counter_bytes(N, H, kv.Hkv, kv.B, c.R) +
+         2ull * sm_count() * c.per_sm * slot_floats(c.R, c.HD) * sizeof(float);
+}
+
+medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const void* q,
+                                       float scale, const TreeDev* tree, const int32_t* starts, void* out, void* ws,
+                                       cudaStream_t stream) {
+  Work w{};
+  w.kv = kv;
+  if (tree) w.t = *tree;
+  w.N = N;
+  w.H = H;
+  w.g = H / kv.Hkv;
+  w.starts = starts;
+  w.status = device_status_ptr();
+  const Choice c = choose(kv, N, H);
+  w.counters = static_cast<unsigned*>(ws);
+  w.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + counter_bytes(N, H, kv.Hkv, kv.B, c.R));
+  const int grid = sm_count() * c.per_sm;
+  const float s = scale * kLog2e;
+  const cudaError_t e = dtype == MEDUSA_BF16 ? run_for<uint16_t>(c, w, grid, q, s, out, stream)
+                                             : run_for<float>(c, w, grid, q, s, out, stream);
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail("medusa_paged_attention", e);
+}
+
+}  // namespace medusa

@@ -1,0 +1,307 @@
+// Rotary positions of new tokens and their place in a paged cache: queries
+// and keys are rotated, keys and values written to their pages, in one pass.
+//
+// Pair i of a head turns by position * f_i.  At position 10^6 the product has
+// an absolute error of 0.06 rad in fp32, so the frequency is kept as a 64-bit
+// fraction of a turn: position * turns modulo 2^64 is the angle by integer
+// wrap-around, exact for any position; its top 32 bits give the angle to
+// 2^-32 turns.  A block computes cos and sin once per (token, pair) into
+// shared memory for all H + Hkv heads.
+//
+// Bound by HBM: every element is read once and written once.
+#include "common.cuh"
+
+namespace medusa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTok = 8;      // tokens per block
+constexpr int kBatch = 4;       // heads a thread loads before it stores any
+
+struct RopeArgs {
+  PagedDev kv;
+  int N, H, rot, half, tok;     // half: MEDUSA_ROPE_HALF
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t qs, ks, vs;
+  void* q_out;
+  const uint64_t* turns;
+  float amplitude;
+  const int32_t* positions;
+  const int32_t* starts;
+  int* status;
+};
+
+// Where a token of the packed list goes: `base` is its element offset inside
+// its page block (head 0), or -1 when it is to be left alone.
+struct Place {
+  long long base;
+  int pos;
+};
+
+__device__ Place place_token(const RopeArgs& a, int n, const int32_t* starts /* shared, or null */) {
+  Place pl{-1, 0};
+  const int B = a.kv.B;
+  int b, first, last;
+  if (starts == nullptr) {
+    const int each = a.N / B;
+    b = n / each;
+    first = b * each;
+    last = first + each;
+  } else {
+    int lo = 0, hi = B;          // largest b with starts[b] <= n
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (starts[mid] <= n) lo = mid; else hi = mid;
+    }
+    b = lo;
+    first = starts[b];
+    last = starts[b + 1];
+    if (n < first || n >= last || last > a.N) return pl;   // behind the last sequence
+  }
+  const int L = a.kv.lens[b];
+  const long long cap = static_cast<long long>(a.kv.max_pages) << a.kv.page_shift;
+  if (L < 0 || static_cast<long long>(L) + (last - first) > cap) {
+    set_device_status(a.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
+    return pl;
+  }
+  const long long row = static_cast<long long>(L) + (n - first);
+  const int page = a.kv.table[static_cast<long long>(b) * a.kv.max_pages + (row >> a.kv.page_shift)];
+  if (page < 0 || page >= a.kv.n_pages) {
+    set_device_status(a.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
+    return pl;
+  }
+  pl.base = ((static_cast<long long>(page) * a.kv.Hkv << a.kv.page_shift) + (row & ((1 << a.kv.page_shift) - 1))) * a.kv.hd;
+  pl.pos = a.positions ? a.positions[n] : static_cast<int>(row);
+  return pl;
+}
+
+template <typename T>
+struct Vec16;
+template <>
+struct Vec16<float> {
+  static constexpr int kE = 4;
+  static __device__ __forceinline__ void unpack(const uint4& w, float* f) {
+    f[0] = __uint_as_float(w.x);
+    f[1] = __uint_as_float(w.y);
+    f[2] = __uint_as_float(w.z);
+    f[3] = __uint_as_float(w.w);
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+  }
+};
+template <>
+struct Vec16<uint16_t> {
+  static constexpr int kE = 8;
+  static __device__ __forceinline__ void unpack(const uint4& w, float* f) {
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = bf16lo(u[i]);
+      f[2 * i + 1] = bf16hi(u[i]);
+    }
+  }
+  static __device__ __forceinline__ uint4 pack(const float* f) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      u[i] = static_cast<uint32_t>(f32_to_bf16_rne(f[2 * i])) | (static_cast<uint32_t>(f32_to_bf16_rne(f[2 * i + 1])) << 16);
+    return make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ float load1(const T* p);
+template <>
+__device__ __forceinline__ float load1<float>(const float* p) { return *p; }
+template <>
+__device__ __forceinline__ float load1<uint16_t>(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(uint16_t* p, float x) { *p = f32_to_bf16_rne(x); }
+
+// Shared per block: the tokens' places and their cos / sin (times amplitude).
+template <typename T>
+__device__ int prepare_tokens(const RopeArgs& a, int n0, Place* place, float2* cs) {
+  __shared__ int32_t starts[MEDUSA_MAX_B + 1];
+  const int tid = threadIdx.x, B = a.kv.B;
+  if (a.starts) {
+    for (int i = tid; i <= B; i += kThreads) starts[i] = a.starts[i];
+    __syncthreads();
+    if (blockIdx.x == 0 && tid < B && (starts[tid] < 0 || starts[tid + 1] < starts[tid] || starts[tid + 1] > a.N))
+      set_device_status(a.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
+  }
+  const int count = min(a.tok, a.N - n0);
+  if (tid < count) place[tid] = place_token(a, n0 + tid, a.starts ? starts : nullptr);
+  __syncthreads();
+  const int pairs = a.rot >> 1;
+  for (int x = tid; x < count * pairs; x += kThreads) {
+    const int t = x / pairs, i = x - t * pairs;
+    const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(place[t].pos)) * a.turns[i];
+    float s, c;
+    sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f /* 2^-31: half turns */, &s, &c);
+    cs[x] = make_float2(c * a.amplitude, s * a.amplitude);
+  }
+  __syncthreads();
+  return count;
+}
+
+// 16-byte path: a thread owns vector j of a head (in the half layout also its
+// partner rot/2 further on) and walks the heads of a token.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_append_vec(const RopeArgs a) {
+  constexpr int E = Vec16<T>::kE;
+  extern __shared__ float2 cs[];
+  __shared__ Place place[kMaxTok];
+  const int n0 = blockIdx.x * a.tok;
+  const int count = prepare_tokens<T>(a, n0, place, cs);
+  const int hd = a.kv.hd, H = a.H, Hkv = a.kv.Hkv;
+  const int turned = a.half ? (a.rot >> 1) / E : a.rot / E;   // units that rotate
+  const int units = turned + (hd - a.rot) / E;
+  const int per = kThreads / units;                           // heads per sweep
+  const int h0 = threadIdx.x / units, j = threadIdx.x - h0 * units;
+  if (h0 >= per) return;
+  const bool two = a.half && j < turned;
+  const int va = j < turned ? j * E : a.rot + (j - turned) * E;   // element offset of the (first) vector
+  const int vb = va + (a.rot >> 1);
+  const int heads = H + 2 * Hkv;
+  const long long page_head = static_cast<long long>(hd) << a.kv.page_shift;
+  for (int t = 0; t < count; ++t) {
+    const long long base = place[t].base;
+    if (base < 0) continue;
+    const long long n = n0 + t;
+    const float2* tcs = cs + t * (a.rot >> 1);
+    for (int hb = h0; hb < heads; hb += kBatch * per) {
+      uint4 x[kBatch], y[kBatch];
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m) {
+        const int h = hb + m * per;
+        if (h >= heads) continue;
+        const T* src = h < H ? static_cast<const T*>(a.q) + n * a.qs + static_cast<long long>(h) * hd
+                       : h < H + Hkv ? static_cast<const T*>(a.k) + n * a.ks + static_cast<long long>(h - H) * hd
+                                     : static_cast<const T*>(a.v) + n * a.vs + static_cast<long long>(h - H - Hkv) * hd;
+        x[m] = *reinterpret_cast<const uint4*>(src + va);
+        if (two) y[m] = *reinterpret_cast<const uint4*>(src + vb);
+      }
+#pragma unroll
+      for (int m = 0; m < kBatch; ++m) {
+        const int h = hb + m * per;
+        if (h >= heads) continue;
+        T* dst = h < H ? static_cast<T*>(a.q_out) + (n * H + h) * hd
+                 : h < H + Hkv ? static_cast<T*>(a.kv.k) + base + (h - H) * page_head
+                               : static_cast<T*>(a.kv.v) + base + (h - H - Hkv) * page_head;
+        if (j < turned && h < H + Hkv) {
+          float f[E];
+          Vec16<T>::unpack(x[m], f);
+          if (two) {
+            float g[E];
+            Vec16<T>::unpack(y[m], g);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              const float2 w = tcs[va + e];
+              const float p = f[e] * w.x - g[e] * w.y, r = g[e] * w.x + f[e] * w.y;
+              f[e] = p;
+              g[e] = r;
+            }
+            y[m] = Vec16<T>::pack(g);
+          } else {
+#pragma unroll
+            for (int e = 0; e < E; e += 2) {
+              const float2 w = tcs[(va + e) >> 1];
+              const float p = f[e] * w.x - f[e + 1] * w.y, r = f[e + 1] * w.x + f[e] * w.y;
+              f[e] = p;
+              f[e + 1] = r;
+            }
+          }
+          x[m] = Vec16<T>::pack(f);
+        }
+        *reinterpret_cast<uint4*>(dst + va) = x[m];
+        if (two) *reinterpret_cast<uint4*>(dst + vb) = y[m];
+      }
+    }
+  }
+}
+
+// Element path, for rotated parts that 16-byte vectors do not divide.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) rope_append_any(const RopeArgs a) {
+  extern __shared__ float2 cs[];
+  __shared__ Place place[kMaxTok];
+  const int n0 = blockIdx.x * a.tok;
+  const int count = prepare_tokens<T>(a, n0, place, cs);
+  const int hd = a.kv.hd, H = a.H, Hkv = a.kv.Hkv, pairs = a.rot >> 1;
+  const int units = pairs + hd - a.rot;                        // pairs, then single elements
+  const long long page_head = static_cast<long long>(hd) << a.kv.page_shift;
+  for (int t = 0; t < count; ++t) {
+    const long long base = place[t].base;
+    if (base < 0) continue;
+    const long long n = n0 + t;
+    for (int x = threadIdx.x; x < (H + 2 * Hkv) * units; x += kThreads) {
+      const int h = x / units, j = x - h * units;
+      const T* src = h < H ? static_cast<const T*>(a.q) + n * a.qs + static_cast<long long>(h) * hd
+                     : h < H + Hkv ? static_cast<const T*>(a.k) + n * a.ks + static_cast<long long>(h - H) * hd
+                                   : static_cast<const T*>(a.v) + n * a.vs + static_cast<long long>(h - H - Hkv) * hd;
+      T* dst = h < H ? static_cast<T*>(a.q_out) + (n * H + h) * hd
+               : h < H + Hkv ? static_cast<T*>(a.kv.k) + base + (h - H) * page_head
+                             : static_cast<T*>(a.kv.v) + base + (h - H - Hkv) * page_head;
+      if (j >= pairs) {
+        dst[a.rot + j - pairs] = src[a.rot + j - pairs];
+        continue;
+      }
+      const int ia = a.half ? j : 2 * j, ib = a.half ? j + pairs : 2 * j + 1;
+      if (h >= H + Hkv) {
+        dst[ia] = src[ia];
+        dst[ib] = src[ib];
+        continue;
+      }
+      const float f = load1<T>(src + ia), g = load1<T>(src + ib);
+      const float2 w = cs[t * pairs + j];
+      store1(dst + ia, f * w.x - g * w.y);
+      store1(dst + ib, g * w.x + f * w.y);
+    }
+  }
+}
+
+}  // namespace
+
+medusa_status_t launch_rope_append(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const void* q,
+                                   int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                                   void* q_out, const medusa_rotary_t& rotary, const int32_t* positions,
+                                   const int32_t* starts, cudaStream_t stream) {
+  RopeArgs a{};
+  a.kv = kv;
+  a.N = N;
+  a.H = H;
+  a.rot = rotary.rot;
+  a.half = rotary.layout == MEDUSA_ROPE_HALF;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.qs = q_stride;
+  a.ks = k_stride;
+  a.vs = v_stride;
+  a.q_out = q_out;
+  a.turns = rotary.turns;
+  a.amplitude = rotary.amplitude;
+  a.positions = positions;
+  a.starts = starts;
+  a.status = device_status_ptr();
+  const int blocks = 4 * sm_count();
+  a.tok = N / blocks < 1 ? 1 : N / blocks > kMaxTok ? kMaxTok : N / blocks;
+  const int grid = (N + a.tok - 1) / a.tok;
+  const size_t smem = static_cast<size_t>(a.tok) * (a.rot / 2) * sizeof(float2);   // at most 8 KB
+  const int E = dtype == MEDUSA_BF16 ? 8 : 4;
+  const bool vec = (a.half ? a.rot / 2 : a.rot) % E == 0;
+  if (dtype == MEDUSA_BF16) {
+    if (vec) rope_append_vec<uint16_t><<<grid, kThreads, smem, stream>>>(a);
+    else rope_append_any<uint16_t><<<grid, kThreads, smem, stream>>>(a);
+  } else {
+    if (vec) rope_append_vec<float><<<grid, kThreads, smem, stream>>>(a);
+    else rope_append_any<float><<<grid, kThreads, smem, stream>>>(a);
+  }
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail("medusa_rope_append", e);
+}
+
+}  // namespace medusa
