@@ -49,7 +49,7 @@ struct Shape {
 template <typename T, int HD, int R>
 __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(const Work w, const T* q, float scale_log2, T* out) {
   using S = Shape<HD, R>;
-  using C = Cut<R, kBK>;
+  using C = Cut<kBK>;
   constexpr int NT = S::kThreads, RR = S::kRows, DV = HD / 64;   // DV groups of 4 dimensions per thread
   extern __shared__ __align__(16) float sh[];
   float* qs = sh;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       __syncthreads();
       const int c_lo = C::owner(x.start, W), c_hi = C::owner(x.start + x.blocks - 1, W);
       if (tid == 0) {
-        unsigned* ctr = w.counters + static_cast<size_t>(plan.tile0[b] + x.tile) * w.kv.Hkv + x.h;
+        unsigned* ctr = C::counter(w, plan, x);
         s_last = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(c_hi - c_lo);
         if (s_last) *ctr = 0u;
       }
@@ -304,15 +304,19 @@ cudaError_t run_for(const Choice& c, const Work& w, int grid, const void* q, flo
 }  // namespace
 
 size_t paged_attention_workspace_bytes(const PagedDev& kv, medusa_dtype_t dtype, int N, int H) {
-  (void)dtype;
   const Choice c = choose(kv, N, H);
-  return counter_bytes(N, H, kv.Hkv, kv.B, c.R) +
+  const size_t tc = paged_attention_tc_supported(kv, dtype, H) ? paged_attention_tc_workspace_bytes(kv, N, H) : 0;
+  const size_t any = counter_bytes(N, H, kv.Hkv, kv.B, c.R) +
          2ull * sm_count() * c.per_sm * slot_floats(c.R, c.HD) * sizeof(float);
+  return tc > any ? tc : any;      // the scale, known only at the call, decides between the two
 }
 
 medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const void* q,
                                        float scale, const TreeDev* tree, const int32_t* starts, void* out, void* ws,
                                        cudaStream_t stream) {
+  // The tensor-core kernel takes the maximum of the unscaled scores.
+  if (scale > 0.f && paged_attention_tc_supported(kv, dtype, H))
+    return launch_paged_attention_tc(kv, N, H, q, scale, tree, starts, out, ws, stream);
   Work w{};
   w.kv = kv;
   if (tree) w.t = *tree;
@@ -322,6 +326,7 @@ medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype,
   w.starts = starts;
   w.status = device_status_ptr();
   const Choice c = choose(kv, N, H);
+  w.R = c.R;
   w.counters = static_cast<unsigned*>(ws);
   w.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + counter_bytes(N, H, kv.Hkv, kv.B, c.R));
   const int grid = sm_count() * c.per_sm;

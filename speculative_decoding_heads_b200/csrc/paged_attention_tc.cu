@@ -1,0 +1,667 @@
+// Attention of new tokens over a paged cache on the tensor cores: bf16 heads
+// of 64 or 128, any group of up to 128 query heads.
+//
+// A unit (paged_work.cuh) is up to two groups of 128 query rows of one
+// sequence and key head; the cache streams past it in tiles of 128 keys:
+//   S = Q K^T (tcgen05, M 128 x N 128), P = 2^(scale S - m) in registers,
+//   O += P V (P read back from tensor memory), l += sum P, m the running
+// maximum.  Two softmax warpgroups keep the tensor cores busy in turn.  A
+// unit of more than 128 rows gives each warpgroup its own 128 rows and every
+// key tile to both, so a tile's 64 KB from L2 serve 256 rows (prompts: bound
+// by the tensor cores and the exponentials).  A unit of fewer rows gives the
+// key tiles to the warpgroups alternately, each with its own O, m and l
+// (tokens and trees: bound by the cache's bytes); the two are joined with
+// factors 2^(m_w - m) when they are written.
+//
+// The maximum is moved (and O rescaled) only when a tile's exceeds it by more
+// than 2^8: any reference that keeps the exponents finite gives the same
+// quotient.  P is rounded to bf16 for the second product, which costs at most
+// half a bf16 step of each probability; the output, rounded to bf16 itself,
+// has no use for more.  Sums, maxima and O are fp32.
+//
+// Tensor memory (512 columns): S_w at 128 w, its P (two keys per column) over
+// the first half of it, O_w at 256 + 128 w.  P V of a step is issued before
+// the next Q K^T that overwrites P, and tensor-core operations of one thread
+// run in order.
+//
+// Warp 0 loads (TMA, one box per page; the table's entries of a tile are
+// fetched by as many lanes one tile ahead), warp 1 issues the products, warps
+// 4-11 are the two softmax warpgroups, a row per thread.  K and V tiles go
+// through one ring in the order in which they are used.  Every wait is bounded.
+#include <cudaTypedefs.h>
+
+#include "paged_work.cuh"
+#include "tcgen05.cuh"
+
+namespace medusa {
+namespace {
+
+using namespace paged;
+
+constexpr int kBK = 128;                 // keys per tile
+constexpr int kGroup = 128;              // rows per softmax warpgroup
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f;
+
+template <int HD>
+struct Shape {
+  static constexpr int kHalves = HD / 64;
+  static constexpr int kHalf = kBK * 128;                 // 128 rows x 64 elements
+  static constexpr int kTile = kHalves * kHalf;           // a K, V or Q tile
+  static constexpr int kStages = HD == 128 ? 5 : 8;
+  static constexpr int kOffRing = 2 * kTile;              // after two Q tiles
+  static constexpr int kOffBars = kOffRing + kStages * kTile;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  uint64_t q_full[2], q_empty[2];
+  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t stat_full, stat_free, group[2];   // statistics handed over; the threads of one warpgroup
+  uint32_t tmem_base;
+  int abort, last[2];
+  float m1[kGroup], l1[kGroup];          // alternating units: the second warpgroup's statistics
+  Plan plan;
+};
+
+template <int HD>
+constexpr int smem_bytes() { return Shape<HD>::kOffBars + static_cast<int>(sizeof(Bars)); }
+static_assert(smem_bytes<128>() <= 232448, "shared memory budget");
+static_assert(smem_bytes<64>() <= 232448, "shared memory budget");
+
+struct Params {
+  Work w;
+  int rows;                // query rows per group: 128 cut to whole tokens
+  int q_tokens;            // tokens per Q box
+  int box;                 // page rows per TMA box
+  float scale_log2;
+  uint16_t* out;
+};
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, int* status) {
+  if (b->abort) return false;
+  if (mbar_wait(bar, parity)) return true;
+  set_device_status(status, MEDUSA_ERR_TIMEOUT, kDetailPagedWait);
+  b->abort = 1;
+  return false;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// What every role knows of a piece.
+struct Seg {
+  int n;             // key tiles of this piece
+  int rows;          // query rows of the unit
+  bool two;          // both groups have rows: each takes every tile
+};
+
+__device__ __forceinline__ Seg segment(const Params& p, const Plan& pl, const Piece& x) {
+  Seg s;
+  s.n = x.kb1 - x.kb0;
+  s.rows = min(p.w.R, pl.n[x.b] * p.w.g - x.tile * p.w.R);
+  s.two = s.rows > p.rows;
+  return s;
+}
+
+using C = Cut<kBK>;
+
+// ---- loads (warp 0) --------------------------------------------------------
+
+template <int HD>
+__device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, const CUtensorMap* v_map, const Params& p,
+                          unsigned char* smem, Bars* bar, Piece x, unsigned long long left) {
+  using S = Shape<HD>;
+  const int lane = threadIdx.x & 31;
+  const Plan& pl = bar->plan;
+  const int sub = kBK / p.box;                         // boxes per half tile
+  const int shift = p.w.kv.page_shift, mask = (1 << shift) - 1;
+  const int none = p.w.kv.n_pages * p.w.kv.Hkv;        // past the last page block: reads as zeros
+  int e = 0, nq[2] = {0, 0};
+  // Block index (page, head) of this lane's box of key tile kb.
+  auto lookup = [&](int b, int h, int kb, int keys) {
+    const int j = kb * kBK + lane * p.box;
+    if (lane >= sub || j >= keys) return none;
+    const int page = p.w.kv.table[static_cast<long long>(b) * p.w.kv.max_pages + (j >> shift)];
+    if (page < 0 || page >= p.w.kv.n_pages) {
+      set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
+      return none;
+    }
+    return page * p.w.kv.Hkv + h;
+  };
+  auto entry = [&](const CUtensorMap* map, int kb, int block) {
+    const int st = e % S::kStages;
+    if (e >= S::kStages && !wait(&bar->empty[st], (e / S::kStages - 1) & 1, bar, p.w.status)) return false;
+    unsigned char* d = smem + S::kOffRing + st * S::kTile;
+    if (lane == 0) mbar_arrive_expect_tx(&bar->full[st], S::kTile);
+    __syncwarp();
+    if (lane < sub) {
+      const int row = (kb * kBK + lane * p.box) & mask;
+#pragma unroll
+      for (int hf = 0; hf < S::kHalves; ++hf)
+        tc::tma_load_4d(d + hf * S::kHalf + lane * p.box * 128, map, 0, row, hf, block, &bar->full[st]);
+    }
+    ++e;
+    return true;
+  };
+  auto query = [&](int w, int b, int h, int row0) {
+    if (nq[w] > 0 && !wait(&bar->q_empty[w], (nq[w] - 1) & 1, bar, p.w.status)) return false;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&bar->q_full[w], S::kHalves * p.w.g * p.q_tokens * 128);
+      for (int hf = 0; hf < S::kHalves; ++hf)
+        tc::tma_load_4d(smem + w * S::kTile + hf * S::kHalf, q_map, 0, h * p.w.g, pl.first[b] + row0 / p.w.g, hf, &bar->q_full[w]);
+    }
+    ++nq[w];
+    return true;
+  };
+  for (bool ok = true; ok;) {
+    const Seg s = segment(p, pl, x);
+    const int keys = static_cast<int>(C::keys(p.w, pl, x.b, x.tile));
+    int cur = lookup(x.b, x.h, x.kb0, keys), next = s.n > 1 ? lookup(x.b, x.h, x.kb0 + 1, keys) : none;
+    ok = query(0, x.b, x.h, x.tile * p.w.R) && (!s.two || query(1, x.b, x.h, x.tile * p.w.R + p.rows));
+    ok = ok && entry(k_map, x.kb0, cur);
+    if (!s.two && s.n > 1) ok = ok && entry(k_map, x.kb0 + 1, next);
+    for (int i = 0; ok && i < s.n; ++i) {
+      const int after = i + 2 < s.n ? lookup(x.b, x.h, x.kb0 + i + 2, keys) : none;
+      ok = entry(v_map, x.kb0 + i, cur);
+      if (s.two) {
+        if (ok && i + 1 < s.n) ok = entry(k_map, x.kb0 + i + 1, next);
+      } else if (ok && i + 2 < s.n) {
+        ok = entry(k_map, x.kb0 + i + 2, after);
+      }
+      cur = next;
+      next = after;
+    }
+    if (!ok || left == 0) break;
+    C::next_piece(p.w, pl, x, left);
+  }
+  // Every copy issued lands before the CTA exits (bounded).
+  for (int st = 0; st < S::kStages; ++st)
+    if (e > st) mbar_wait(&bar->full[st], ((e - 1 - st) / S::kStages) & 1);
+  for (int w = 0; w < 2; ++w)
+    if (nq[w] > 0) mbar_wait(&bar->q_full[w], (nq[w] - 1) & 1);
+}
+
+// ---- products (warp 1, one thread) -----------------------------------------
+
+template <int HD>
+__device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bars* bar, Piece x, unsigned long long left) {
+  using S = Shape<HD>;
+  constexpr uint32_t idS = tc::idesc_bf16_f32(kGroup, kBK, 0);
+  constexpr uint32_t idO = tc::idesc_bf16_f32(kGroup, HD, 1);
+  const Plan& pl = bar->plan;
+  int* status = p.w.status;
+  int e = 0, nq[2] = {0, 0}, np[2] = {0, 0}, piece = 0;
+  auto landed = [&](int entry) { return wait(&bar->full[entry % S::kStages], (entry / S::kStages) & 1, bar, status); };
+  auto scores = [&](int w, int q, int entry) {            // S_w = Q_q K^T
+    tc::fence_after_sync();
+    const uint32_t kb = sbase + S::kOffRing + (entry % S::kStages) * S::kTile, qb = sbase + q * S::kTile;
+#pragma unroll
+    for (int c = 0; c < HD / 16; ++c) {
+      const uint32_t off = (c >> 2) * S::kHalf + (c & 3) * 32;
+      tc::mma_ss(tmem + 128 * w, tc::smem_desc_sw128(qb + off, 16, 1024), tc::smem_desc_sw128(kb + off, 16, 1024), idS, c > 0);
+    }
+    tc::mma_commit(&bar->s_full[w]);
+  };
+  auto values = [&](int w, int entry, bool first) {       // O_w += P_w V
+    if (!wait(&bar->p_full[w], np[w] & 1, bar, status)) return false;
+    ++np[w];
+    if (first && piece > 0 && !wait(&bar->o_free[w], (piece - 1) & 1, bar, status)) return false;
+    if (!landed(entry)) return false;
+    tc::fence_after_sync();
+    const uint32_t vb = sbase + S::kOffRing + (entry % S::kStages) * S::kTile;
+#pragma unroll
+    for (int c = 0; c < kBK / 16; ++c)
+      tc::mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + c * 8, tc::smem_desc_sw128(vb + c * 16 * 128, S::kHalf, 1024), idO,
+                 (!first || c > 0) ? 1u : 0u);
+    tc::mma_commit(&bar->pv_done[w]);
+    return true;
+  };
+  auto release = [&](int entry) { tc::mma_commit(&bar->empty[entry % S::kStages]); };
+  for (;;) {
+    const Seg s = segment(p, pl, x);
+    if (!wait(&bar->q_full[0], nq[0] & 1, bar, status)) return;
+    ++nq[0];
+    if (s.two) {
+      if (!landed(e)) return;
+      scores(0, 0, e);
+      if (!wait(&bar->q_full[1], nq[1] & 1, bar, status)) return;
+      ++nq[1];
+      scores(1, 1, e);
+      release(e++);
+      if (s.n == 1) {
+        tc::mma_commit(&bar->q_empty[0]);
+        tc::mma_commit(&bar->q_empty[1]);
+      }
+      for (int i = 0; i < s.n; ++i) {
+        const int v = e++;
+        if (!values(0, v, i == 0)) return;
+        if (i + 1 < s.n) {
+          if (!landed(e)) return;
+          scores(0, 0, e);
+          if (i + 2 == s.n) tc::mma_commit(&bar->q_empty[0]);
+        }
+        if (!values(1, v, i == 0)) return;
+        release(v);
+        if (i + 1 < s.n) {
+          scores(1, 1, e);
+          if (i + 2 == s.n) tc::mma_commit(&bar->q_empty[1]);
+          release(e++);
+        }
+      }
+    } else {
+      for (int i = 0; i < 2 && i < s.n; ++i) {
+        if (!landed(e)) return;
+        scores(i, 0, e);
+        release(e++);
+      }
+      if (s.n <= 2) tc::mma_commit(&bar->q_empty[0]);
+      for (int i = 0; i < s.n; ++i) {
+        if (!values(i & 1, e, i < 2)) return;
+        release(e++);
+        if (i + 2 < s.n) {
+          if (!landed(e)) return;
+          scores(i & 1, 0, e);
+          release(e++);
+          if (i + 3 == s.n) tc::mma_commit(&bar->q_empty[0]);
+        }
+      }
+    }
+    ++piece;
+    if (left == 0) return;
+    C::next_piece(p.w, pl, x, left);
+  }
+}
+
+// ---- softmax and output (warps 4-11) ----------------------------------------
+
+// Bits o .. o + 63 (o >= 0) of an ancestor-mask row of four words.
+__device__ __forceinline__ uint64_t anc_window(const uint64_t (&a)[4], int o) {
+  if (o >= 256) return 0ull;
+  const int wi = o >> 6, sh = o & 63;
+  const uint64_t w0 = wi == 0 ? a[0] : wi == 1 ? a[1] : wi == 2 ? a[2] : a[3];
+  const uint64_t w1 = wi == 0 ? a[1] : wi == 1 ? a[2] : wi == 2 ? a[3] : 0ull;
+  return sh == 0 ? w0 : (w0 >> sh) | (w1 << (64 - sh));
+}
+// Bits of 64 keys starting at key d rows before (d > 0) or after (d <= 0) the
+// prefix's end: the prefix, then the row's ancestors and itself.
+__device__ __forceinline__ uint64_t tree_bits(const uint64_t (&a)[4], int d) {
+  if (d >= 64) return ~0ull;
+  return d > 0 ? ((1ull << d) - 1ull) | (a[0] << d) : anc_window(a, -d);
+}
+
+template <int HD>
+__device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem, Bars* bar, Piece x, unsigned long long left,
+                            unsigned long long W) {
+  using S = Shape<HD>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = (warp - 4) >> 2;             // softmax warpgroup
+  const int quarter = warp & 3;              // tensor-memory lanes of this warp
+  const int row = 32 * quarter + lane;       // row of the group
+  const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
+  const uint32_t tS = tmem + lanes + 128 * w;
+  const Plan& pl = bar->plan;
+  int* status = p.w.status;
+  int steps = 0;                             // tiles this warpgroup has taken
+  int pv[2] = {0, 0};                        // P V products of both warpgroups before this piece
+  int entries = 0;                           // ring entries before this piece
+  int syncs = 0;                             // uses of this warpgroup's barrier
+  int singles = 0;                           // alternating pieces before this one
+  for (;;) {
+    const Seg s = segment(p, pl, x);
+    const int b = x.b, L = pl.L[b], n = pl.n[b];
+    const int grp_row = x.tile * p.w.R + (s.two ? w * p.rows : 0);   // this group's first row
+    const int rows = s.two ? (w == 0 ? p.rows : s.rows - p.rows) : s.rows;
+    const bool active = 32 * quarter < rows; // a warp without rows only keeps the barriers going
+    const int tok = (grp_row + row) / p.w.g;
+    const int keys = static_cast<int>(C::keys(p.w, pl, b, x.tile));
+    const bool tree = p.w.t.T > 0;
+    uint64_t anc[4] = {0ull, 0ull, 0ull, 0ull};
+    if (tree && row < rows) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < p.w.t.W) anc[i] = p.w.t.anc[tok * p.w.t.W + i];
+    }
+    // Keys below this row's limit are visible (chunks); a tile below every row's limit needs no mask.
+    const int limit = L + min(tok, n - 1) + 1;
+    const int clear = tree ? L : L + grp_row / p.w.g + 1;
+    float m = -INFINITY, l = 0.f;
+    for (int i = s.two ? 0 : w; i < s.n; i += s.two ? 1 : 2, ++steps) {
+      if (!wait(&bar->s_full[w], steps & 1, bar, status)) return;
+      tc::fence_after_sync();
+      const int j0 = (x.kb0 + i) * kBK;
+      if (active) {
+        float sv[kBK];
+#pragma unroll
+        for (int c = 0; c < kBK; c += 32) tc::tmem_ld32(tS + c, sv + c);
+        tc::tmem_wait_ld();
+        if (j0 + kBK > clear) {
+          if (tree) {
+            const uint64_t a = tree_bits(anc, L - j0), c = tree_bits(anc, L - j0 - 64);
+            const uint32_t bits[4] = {static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), static_cast<uint32_t>(c),
+                                      static_cast<uint32_t>(c >> 32)};
+#pragma unroll
+            for (int k = 0; k < kBK; ++k) sv[k] = ((bits[k >> 5] >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
+          } else {
+            const int lim = limit - j0;
+#pragma unroll
+            for (int k = 0; k < kBK; ++k) sv[k] = k < lim ? sv[k] : -INFINITY;
+          }
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int k = 0; k < kBK; ++k) mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
+        const float tm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        float factor = 1.f;
+        if (tm > m + kRescaleLog2 || (m == -INFINITY && tm > -INFINITY)) {
+          factor = m == -INFINITY ? 0.f : tc::ex2_ftz(m - tm);
+          m = tm;
+        }
+        const float ref = m == -INFINITY ? 0.f : -m;
+        const bool first = s.two ? i == 0 : i < 2;
+        // O is rescaled before P is handed over; P V of the step before is done (S was issued after it).
+        if (!first && __any_sync(0xffffffffu, factor != 1.f)) {
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            tc::tmem_ld32(tmem + lanes + 256 + 128 * w + c, o);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] *= factor;
+            tc::tmem_st32(tmem + lanes + 256 + 128 * w + c, o);
+          }
+        }
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kBK; c += 32) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float a = tc::ex2_ftz(fmaf(sv[c + k], p.scale_log2, ref)), d = tc::ex2_ftz(fmaf(sv[c + k + 1], p.scale_log2, ref));
+            sum[k & 2] += a;
+            sum[(k & 2) + 1] += d;
+            pk[k / 2] = pack2(a, d);
+          }
+          tc::tmem_st16(tS + c / 2, pk);
+        }
+        l = l * factor + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        tc::tmem_wait_st();
+      }
+      if ((w == 0 || !s.two) && x.kb0 + i == x.blocks - 1 && (keys & (p.box - 1)) != 0) {
+        // Rows of the last page past the sequence may hold anything: zero
+        // their values, so that 0 * (stale value) stays 0.
+        const int v = entries + 2 * s.n - 1;            // a piece's last ring entry
+        if (!wait(&bar->full[v % S::kStages], (v / S::kStages) & 1, bar, status)) return;
+        const int r0 = keys - j0, r1 = (r0 + p.box - 1) & ~(p.box - 1);
+        unsigned char* d = smem + S::kOffRing + (v % S::kStages) * S::kTile + r0 * 128;
+        for (int c = row; c < (r1 - r0) * 8; c += kGroup)
+#pragma unroll
+          for (int hf = 0; hf < S::kHalves; ++hf) *reinterpret_cast<uint4*>(d + hf * S::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+        tc::fence_proxy_async_smem();
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar->p_full[w]);
+    }
+
+    // Output, a row per thread.  Where the tiles alternated, the second
+    // warpgroup hands over its statistics and the first joins and writes both.
+    const int n0 = s.two ? s.n : (s.n + 1) / 2, n1 = s.two ? s.n : s.n / 2;
+    entries += 2 * s.n;
+    bool second = false;                       // O_1 belongs to this thread's row as well
+    float f0 = 1.f, f1 = 0.f;
+    if (!s.two) {
+      if (w == 1) {
+        // the statistics before these have been read
+        if (singles > 0 && !wait(&bar->stat_free, (singles - 1) & 1, bar, status)) return;
+        bar->m1[row] = m;
+        bar->l1[row] = l;
+        tc::mbar_arrive(&bar->stat_full);
+      } else {
+        if (!wait(&bar->stat_full, singles & 1, bar, status)) return;
+        const float m1 = bar->m1[row], l1 = bar->l1[row], mm = fmaxf(m, m1);
+        tc::mbar_arrive(&bar->stat_free);
+        f0 = m == -INFINITY ? 0.f : tc::ex2_ftz(m - mm);
+        f1 = m1 == -INFINITY ? 0.f : tc::ex2_ftz(m1 - mm);
+        m = mm;
+        l = f0 * l + f1 * l1;
+        second = n1 > 0;
+      }
+      ++singles;
+    }
+    if (s.two || w == 0) {
+      if (!wait(&bar->pv_done[w], (pv[w] + (w == 0 ? n0 : n1) - 1) & 1, bar, status)) return;
+      if (second && !wait(&bar->pv_done[1], (pv[1] + n1 - 1) & 1, bar, status)) return;
+      tc::fence_after_sync();
+      const bool whole = C::whole(x);
+      const int slot_row = (s.two ? w * kGroup : 0) + row;           // rows of a slot: 2 * kGroup
+      float* slot = p.w.slots + C::slot(blockIdx.x, x.start, W) * slot_floats(2 * kGroup, HD);
+      uint16_t* dst = p.out + (static_cast<size_t>(pl.first[b] + tok) * p.w.H + x.h * p.w.g + (grp_row + row - tok * p.w.g)) * HD;
+      const float inv = 1.f / l;
+      auto put = [&](int c, const float (&o)[32], float by) {
+        if (row >= rows) return;
+#pragma unroll
+        for (int k = 0; k < 32; k += 8)
+          *reinterpret_cast<uint4*>(dst + c + k) =
+              make_uint4(pack2(o[k] * by, o[k + 1] * by), pack2(o[k + 2] * by, o[k + 3] * by),
+                         pack2(o[k + 4] * by, o[k + 5] * by), pack2(o[k + 6] * by, o[k + 7] * by));
+      };
+      if (active) {
+#pragma unroll 1
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          tc::tmem_ld32(tmem + lanes + 256 + 128 * w + c, o);
+          tc::tmem_wait_ld();
+          if (second) {
+            float o1[32];
+            tc::tmem_ld32(tmem + lanes + 384 + c, o1);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], f1, o[k] * f0);
+          }
+          if (whole) {
+            put(c, o, inv);
+          } else {
+            float4* d = reinterpret_cast<float4*>(slot + 4 * kGroup) + (c / 4) * (2 * kGroup) + slot_row;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) __stcg(d + k * (2 * kGroup), make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+          }
+        }
+      }
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(&bar->o_free[w]);
+        if (!s.two) tc::mbar_arrive(&bar->o_free[1]);
+      }
+      if (!whole) {
+        if (active) {
+          __stcg(slot + slot_row, m);
+          __stcg(slot + 2 * kGroup + slot_row, l);
+        }
+        __threadfence();
+        tc::mbar_arrive(&bar->group[w]);
+        if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
+        const int lo = C::owner(x.start, W), hi = C::owner(x.start + x.blocks - 1, W);
+        if (row == 0) {
+          unsigned* ctr = C::counter(p.w, pl, x) + w;
+          bar->last[w] = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(hi - lo);
+          if (bar->last[w]) *ctr = 0u;
+        }
+        tc::mbar_arrive(&bar->group[w]);
+        if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
+        if (bar->last[w] && active) {
+          __threadfence();
+          auto at = [&](int c) { return p.w.slots + C::slot(c, x.start, W) * slot_floats(2 * kGroup, HD); };
+          float mm = -INFINITY, ll = 0.f;
+          for (int c = lo; c <= hi; ++c) mm = fmaxf(mm, __ldcg(at(c) + slot_row));
+          const float ref = mm == -INFINITY ? 0.f : mm;
+          for (int c = lo; c <= hi; ++c) ll += tc::ex2_ftz(__ldcg(at(c) + slot_row) - ref) * __ldcg(at(c) + 2 * kGroup + slot_row);
+#pragma unroll 1
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = 0.f;
+            for (int y = lo; y <= hi; ++y) {
+              const float f = tc::ex2_ftz(__ldcg(at(y) + slot_row) - ref);
+              const float4* d = reinterpret_cast<const float4*>(at(y) + 4 * kGroup) + (c / 4) * (2 * kGroup) + slot_row;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float4 v = __ldcg(d + k * (2 * kGroup));
+                o[4 * k] = fmaf(f, v.x, o[4 * k]);
+                o[4 * k + 1] = fmaf(f, v.y, o[4 * k + 1]);
+                o[4 * k + 2] = fmaf(f, v.z, o[4 * k + 2]);
+                o[4 * k + 3] = fmaf(f, v.w, o[4 * k + 3]);
+              }
+            }
+            put(c, o, 1.f / ll);
+          }
+        }
+      }
+    }
+    pv[0] += n0;
+    pv[1] += n1;
+    if (left == 0) return;
+    C::next_piece(p.w, pl, x, left);
+  }
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_attn_tc(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ CUtensorMap k_map,
+                  const __grid_constant__ CUtensorMap v_map, const Params p) {
+  using S = Shape<HD>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  if ((smem_u32(smem) & 1023u) != 0u) {      // the swizzle pattern needs it; no static shared memory precedes it
+    if (threadIdx.x == 0) set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedWait);
+    return;
+  }
+  Bars* bar = reinterpret_cast<Bars*>(smem + S::kOffBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int st = 0; st < S::kStages; ++st) {
+      mbar_init(&bar->full[st], 1);
+      mbar_init(&bar->empty[st], 1);
+    }
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(&bar->q_full[w], 1);
+      mbar_init(&bar->q_empty[w], 1);
+      mbar_init(&bar->s_full[w], 1);
+      mbar_init(&bar->p_full[w], 4);
+      mbar_init(&bar->pv_done[w], 1);
+      mbar_init(&bar->o_free[w], 4);
+      mbar_init(&bar->group[w], kGroup);
+    }
+    mbar_init(&bar->stat_full, kGroup);
+    mbar_init(&bar->stat_free, kGroup);
+    bar->abort = 0;
+    fence_barrier_init();
+    tc::prefetch_tensormap(&q_map);
+    tc::prefetch_tensormap(&k_map);
+    tc::prefetch_tensormap(&v_map);
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(&bar->tmem_base, kTmemCols);
+    tc::tmem_relinquish();
+  }
+  unsigned long long begin, end;
+  int b0 = 0, h0 = 0;
+  C::plan<kThreads>(p.w, bar->plan, &begin, &end, &b0, &h0);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = bar->tmem_base;
+  if (begin < end) {
+    unsigned long long left = end - begin;
+    const Piece x = C::first_piece(p.w, bar->plan, begin, b0, h0, left);
+    if (warp == 0) {
+      run_loads<HD>(&q_map, &k_map, &v_map, p, smem, bar, x, left);
+    } else if (warp == 1) {
+      if (lane == 0) run_products<HD>(p, smem_u32(smem), tmem, bar, x, left);
+    } else if (warp >= 4) {
+      run_softmax<HD>(p, smem, tmem, bar, x, left, bar->plan.before[p.w.kv.B]);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int HD>
+medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float scale, const TreeDev* tree,
+                       const int32_t* starts, void* out, void* ws, cudaStream_t stream) {
+  using S = Shape<HD>;
+  auto enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(tensor_map_encoder());
+  if (!enc) return fail(MEDUSA_ERR_UNSUPPORTED, "medusa_paged_attention: cuTensorMapEncodeTiled unavailable");
+  Params p{};
+  p.w.kv = kv;
+  if (tree) p.w.t = *tree;
+  p.w.N = N;
+  p.w.H = H;
+  p.w.g = H / kv.Hkv;
+  p.w.starts = starts;
+  p.w.status = device_status_ptr();
+  const int tokens = kGroup / p.w.g;
+  p.rows = tokens * p.w.g;
+  p.w.R = 2 * p.rows;
+  const int most = starts ? N : N / kv.B;                // tokens of one sequence
+  p.q_tokens = tokens < most ? tokens : most;
+  const int page = 1 << kv.page_shift;
+  p.box = page < kBK ? page : kBK;
+  p.scale_log2 = scale * kLog2e;
+  p.out = static_cast<uint16_t*>(out);
+  p.w.counters = static_cast<unsigned*>(ws);
+  p.w.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + counter_bytes(N, H, kv.Hkv, kv.B, p.w.R));
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  CUtensorMap qm, km, vm;
+  {
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(H), static_cast<cuuint64_t>(N), S::kHalves};
+    const cuuint64_t strides[3] = {HD * 2, static_cast<cuuint64_t>(H) * HD * 2, 128};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.w.g), static_cast<cuuint32_t>(p.q_tokens), 1};
+    if (enc(&qm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(q), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return fail(MEDUSA_ERR_UNSUPPORTED, "medusa_paged_attention: q tensor map rejected");
+  }
+  for (int which = 0; which < 2; ++which) {
+    const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(page), S::kHalves, static_cast<cuuint64_t>(kv.n_pages) * kv.Hkv};
+    const cuuint64_t strides[3] = {HD * 2, 128, static_cast<cuuint64_t>(page) * HD * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.box), 1, 1};
+    if (enc(which ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, which ? kv.v : kv.k, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return fail(MEDUSA_ERR_UNSUPPORTED, "medusa_paged_attention: page tensor map rejected");
+  }
+  cudaError_t e = cudaFuncSetAttribute(paged_attn_tc<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<HD>());
+  if (e == cudaSuccess)
+    e = launch_kernel(paged_attn_tc<HD>, dim3(sm_count()), dim3(kThreads), smem_bytes<HD>(), stream, false, qm, km, vm, p);
+  return e == cudaSuccess ? MEDUSA_OK : cuda_fail("medusa_paged_attention: tcgen05 launch", e);
+}
+
+}  // namespace
+
+bool paged_attention_tc_supported(const PagedDev& kv, medusa_dtype_t dtype, int H) {
+  return dtype == MEDUSA_BF16 && (kv.hd == 64 || kv.hd == 128) && H / kv.Hkv <= kGroup &&
+         static_cast<long long>(kv.n_pages) * kv.Hkv < 0x7fffffffll;
+}
+
+size_t paged_attention_tc_workspace_bytes(const PagedDev& kv, int N, int H) {
+  const int g = H / kv.Hkv;
+  return counter_bytes(N, H, kv.Hkv, kv.B, 2 * (kGroup / g) * g) + 2ull * sm_count() * slot_floats(2 * kGroup, kv.hd) * sizeof(float);
+}
+
+medusa_status_t launch_paged_attention_tc(const PagedDev& kv, int N, int H, const void* q, float scale, const TreeDev* tree,
+                                          const int32_t* starts, void* out, void* ws, cudaStream_t stream) {
+  return kv.hd == 128 ? launch<128>(kv, N, H, q, scale, tree, starts, out, ws, stream)
+                      : launch<64>(kv, N, H, q, scale, tree, starts, out, ws, stream);
+}
+
+}  // namespace medusa

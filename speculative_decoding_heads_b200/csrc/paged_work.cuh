@@ -17,12 +17,15 @@
 namespace medusa {
 namespace paged {
 
+constexpr int kCounters = 2;   // per unit: row groups that are joined on their own
+
 struct Work {
   PagedDev kv;
   TreeDev t;               // T = 0: causal chunks
   int N, H, g;             // g = H / Hkv
+  int R;                   // query rows per tile
   const int32_t* starts;
-  unsigned* counters;      // one per unit, zero between calls
+  unsigned* counters;      // kCounters per unit, zero between calls
   float* slots;            // 2 per CTA
   int* status;
 };
@@ -30,9 +33,8 @@ struct Work {
 struct Plan {
   int L[MEDUSA_MAX_B], n[MEDUSA_MAX_B], first[MEDUSA_MAX_B];
   int tile0[MEDUSA_MAX_B + 1];                  // tiles of the sequences before
-  unsigned long long per_head[MEDUSA_MAX_B];    // key blocks of one head of the sequence
-  unsigned long long before[MEDUSA_MAX_B + 1];  // key blocks of the sequences before
-  unsigned long long scan[33];
+  unsigned long long before[MEDUSA_MAX_B + 1];  // key blocks of the sequences before, all heads
+  unsigned long long scan[12];
   int tile, block;                              // where this CTA starts
 };
 
@@ -43,16 +45,16 @@ struct Piece {
   unsigned long long start;    // offset of the unit in the whole list
 };
 
-template <int R, int BK>
+template <int BK>
 struct Cut {
-  static __device__ __forceinline__ int tiles(int n, int g) {
-    return static_cast<int>((static_cast<long long>(n) * g + R - 1) / R);
+  static __device__ __forceinline__ int tiles(const Work& w, int n) {
+    return static_cast<int>((static_cast<long long>(n) * w.g + w.R - 1) / w.R);
   }
   // Rows of the cache that the tile's last row can see.
   static __device__ __forceinline__ long long keys(const Work& w, const Plan& p, int b, int tile) {
     const int n = p.n[b];
     if (w.t.T > 0) return static_cast<long long>(p.L[b]) + n;
-    const int last = static_cast<int>((static_cast<long long>(tile + 1) * R - 1) / w.g) + 1;
+    const int last = static_cast<int>((static_cast<long long>(tile + 1) * w.R - 1) / w.g) + 1;
     return static_cast<long long>(p.L[b]) + (last < n ? last : n);
   }
   static __device__ __forceinline__ int blocks(const Work& w, const Plan& p, int b, int tile) {
@@ -87,11 +89,11 @@ struct Cut {
       p.L[tid] = L;
       p.n[tid] = n;
       p.first[tid] = first;
-      p.per_head[tid] = 0ull;
+      p.before[tid + 1] = 0ull;              // first: key blocks of one head of the sequence
     }
     __syncthreads();
     if (tid < 32) {
-      const int x = tiles(p.n[2 * lane], w.g), y = tiles(p.n[2 * lane + 1], w.g);
+      const int x = tiles(w, p.n[2 * lane]), y = tiles(w, p.n[2 * lane + 1]);
       int s = x + y;
       for (int o = 1; o < 32; o <<= 1) {
         const int v = __shfl_up_sync(0xffffffffu, s, o);
@@ -109,12 +111,12 @@ struct Cut {
         const int mid = (lo + hi) >> 1;
         if (p.tile0[mid] <= t) lo = mid; else hi = mid;
       }
-      atomicAdd(&p.per_head[lo], static_cast<unsigned long long>(blocks(w, p, lo, t - p.tile0[lo])));
+      atomicAdd(&p.before[lo + 1], static_cast<unsigned long long>(blocks(w, p, lo, t - p.tile0[lo])));
     }
     __syncthreads();
     if (tid < 32) {
       const unsigned long long hk = w.kv.Hkv;
-      const unsigned long long x = p.per_head[2 * lane] * hk, y = p.per_head[2 * lane + 1] * hk;
+      const unsigned long long x = p.before[2 * lane + 1] * hk, y = p.before[2 * lane + 2] * hk;
       unsigned long long s = x + y;
       for (int o = 1; o < 32; o <<= 1) {
         const unsigned long long v = __shfl_up_sync(0xffffffffu, s, o);
@@ -137,9 +139,10 @@ struct Cut {
       if (p.before[mid] <= *begin) lo = mid; else hi = mid;
     }
     unsigned long long rem = *begin - p.before[lo];
+    const unsigned long long per_head = (p.before[lo + 1] - p.before[lo]) / w.kv.Hkv;
     *b_out = lo;
-    *h_out = static_cast<int>(rem / p.per_head[lo]);
-    rem -= *h_out * p.per_head[lo];
+    *h_out = static_cast<int>(rem / per_head);
+    rem -= *h_out * per_head;
     const int nt = p.tile0[lo + 1] - p.tile0[lo];
     if (nt == 1) {
       if (tid == 0) {
@@ -220,17 +223,20 @@ struct Cut {
   static __device__ __forceinline__ int owner(unsigned long long off, unsigned long long W) {
     return static_cast<int>(((off + 1) * ranges(W) - 1) / W);
   }
+  static __device__ __forceinline__ unsigned* counter(const Work& w, const Plan& p, const Piece& x) {
+    return w.counters + (static_cast<size_t>(p.tile0[x.b] + x.tile) * w.kv.Hkv + x.h) * kCounters;
+  }
   // Which of CTA c's two slots holds its piece of the unit starting at `start`.
   static __device__ __forceinline__ int slot(int c, unsigned long long start, unsigned long long W) {
     return 2 * c + (start < W * static_cast<unsigned long long>(c) / ranges(W) ? 0 : 1);
   }
 };
 
-// Bytes of the counters (one per unit of the largest possible number) and of
-// the slots (R rows of hd outputs, a maximum and a sum).
+// Bytes of the counters (for the largest possible number of units) and floats
+// of a slot (R rows of hd outputs, a maximum and a sum).
 inline size_t counter_bytes(int N, int H, int Hkv, int B, int R) {
   const long long tiles = (static_cast<long long>(N) * (H / Hkv) + R - 1) / R + B;
-  return align_up(static_cast<size_t>(tiles) * Hkv * sizeof(unsigned), 256);
+  return align_up(static_cast<size_t>(tiles) * Hkv * kCounters * sizeof(unsigned), 256);
 }
 constexpr size_t slot_floats(int R, int hd) { return static_cast<size_t>(R) * (hd + 2); }
 
