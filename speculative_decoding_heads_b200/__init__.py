@@ -671,6 +671,31 @@ def medusa_generate(tree: Tree, model: Decoder, W1, b1, Wout, prompt, n_new: int
 # a paged cache, and the requests' logits
 # ---------------------------------------------------------------------------
 
+# These calls serve single tokens, where a few microseconds of argument checks
+# on the host would be most of the call: each tensor is looked at once.
+
+
+def _arg(name: str, t, shape: tuple, dtype: torch.dtype, dev: int) -> int:
+    """Device pointer of a contiguous tensor of this shape and dtype on device ``dev``; refusals as
+    ``_spec`` and ``_p`` (a tensor on the host has device -1)."""
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        _spec(name, t, shape, dtype)
+    if t.get_device() != dev:
+        _p(t)
+    return t.data_ptr()
+
+
+def _device_of(t: torch.Tensor) -> int:
+    """Index of the current device, which a CUDA tensor must be on; -1 (no device) for a host tensor,
+    so that its call reports what else is wrong with its arguments first."""
+    return torch.cuda.current_device() if t.is_cuda else -1
+
+
+def _stream_ptr(stream, dev: int) -> int:
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)   # torch.cuda.current_stream() builds a Python object for it
+
 
 class PagedKV:
     """The paged K/V cache of B sequences (``medusa_paged_kv_t``): k_pages, v_pages [layers, n_pages,
@@ -694,6 +719,7 @@ class PagedKV:
                  "the pages, the page table and the lengths must be on one device")
         self.c = PagedKVArgs(dtype, *k_pages.shape, k_pages.data_ptr(), v_pages.data_ptr(), B, page_table.shape[1],
                              page_table.data_ptr(), seq_lens.data_ptr())
+        self.ref = ctypes.byref(self.c)
 
 
 class Rotary:
@@ -706,6 +732,7 @@ class Rotary:
         self.turns = torch.tensor([t - (t >> 63 << 64) for t in turns], dtype=torch.int64, device="cuda")
         self.layout, self.rot, self.amplitude = int(layout), int(rot), amplitude
         self.c = RotaryArgs(self.layout, self.rot, _p(self.turns).value, amplitude)
+        self.ref = ctypes.byref(self.c)
 
 
 def medusa_rotary_turns(rot: int, base: float = 10000.0, scaling: int = MEDUSA_ROPE_NONE, factor: float = 1.0,
@@ -718,22 +745,28 @@ def medusa_rotary_turns(rot: int, base: float = 10000.0, scaling: int = MEDUSA_R
     return list(turns), amplitude.value
 
 
-def _token_rows(name: str, t, heads: int, hd: int, dtype):
-    """(token stride in elements) of a [N, heads, hd] tensor whose heads are dense."""
-    _require(isinstance(t, torch.Tensor) and t.dim() == 3 and t.shape[1:] == (heads, hd),
-             f"{name} must be [N, {heads}, {hd}]")
-    _require(t.dtype == dtype, f"{name} has dtype {t.dtype}, expected {dtype}")
-    _require((t.stride(2) == 1 or hd == 1) and (t.stride(1) == hd or heads == 1),
-             f"the heads of a token of {name} must be dense")
-    return t.stride(0) if t.shape[0] > 1 else heads * hd
+def _on(t: torch.Tensor, dev: int):
+    if t.get_device() != dev or dev < 0:
+        _p(t)
 
 
-def _chunk_starts(kv: PagedKV, N: int, chunk_starts):
+def _token_rows(name: str, t, N: int, heads: int, kv: "PagedKV", dev: int):
+    """(pointer, token stride in elements) of a [N, heads, hd] tensor whose heads are dense."""
+    _require(isinstance(t, torch.Tensor) and t.shape == (N, heads, kv.hd), f"{name} must be [{N}, {heads}, {kv.hd}]")
+    _require(t.dtype == kv.dtype, f"{name} has dtype {t.dtype}, expected {kv.dtype}")
+    s0, s1, s2 = t.stride()
+    _require(s2 == 1 and (s1 == kv.hd or heads == 1), f"the heads of a token of {name} must be dense")
+    if t.get_device() != dev:
+        _p(t)
+    return t.data_ptr(), s0 if N > 1 else heads * kv.hd
+
+
+def _chunk_starts(kv: "PagedKV", N: int, chunk_starts, dev: int):
     _require(N >= 1, "at least one token")
     if chunk_starts is None:
         _require(N % kv.B == 0, "without chunk_starts every sequence has N / B tokens")
-    else:
-        _spec("chunk_starts", chunk_starts, (kv.B + 1,), torch.int32)
+        return None
+    return _arg("chunk_starts", chunk_starts, (kv.B + 1,), torch.int32, dev)
 
 
 def medusa_rope_append(kv: PagedKV, layer: int, q, k, v, q_out, rotary: Rotary, positions=None, chunk_starts=None,
@@ -744,22 +777,21 @@ def medusa_rope_append(kv: PagedKV, layer: int, q, k, v, q_out, rotary: Rotary, 
     the cache rows; chunk_starts [B+1] int32: ragged chunks, else N / B tokens each."""
     _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be [N, H, hd]")
     N, H, _ = q.shape
-    qs = _token_rows("q", q, H, kv.hd, kv.dtype)
-    ks = _token_rows("k", k, kv.Hkv, kv.hd, kv.dtype)
-    vs = _token_rows("v", v, kv.Hkv, kv.hd, kv.dtype)
-    _require(k.shape[0] == N and v.shape[0] == N, "q, k and v must hold the same tokens")
-    _spec("q_out", q_out, (N, H, kv.hd), kv.dtype)
-    _chunk_starts(kv, N, chunk_starts)
-    if positions is not None:
-        _spec("positions", positions, (N,), torch.int32)
-    _p(kv.k_pages)
-    _p(rotary.turns)
-    _check(_lib.medusa_rope_append(ctypes.byref(kv.c), int(layer), N, H, _p(q), qs, _p(k), ks, _p(v), vs, _p(q_out),
-                                   ctypes.byref(rotary.c), _p(positions), _p(chunk_starts), _stream(stream)))
+    dev = _device_of(kv.k_pages)
+    qp, qs = _token_rows("q", q, N, H, kv, dev)
+    kp, ks = _token_rows("k", k, N, kv.Hkv, kv, dev)
+    vp, vs = _token_rows("v", v, N, kv.Hkv, kv, dev)
+    op = _arg("q_out", q_out, (N, H, kv.hd), kv.dtype, dev)
+    st = _chunk_starts(kv, N, chunk_starts, dev)
+    pos = None if positions is None else _arg("positions", positions, (N,), torch.int32, dev)
+    _on(kv.k_pages, dev)
+    _on(rotary.turns, dev)
+    _check(_lib.medusa_rope_append(kv.ref, int(layer), N, H, qp, qs, kp, ks, vp, vs, op, rotary.ref, pos, st,
+                                   _stream_ptr(stream, dev)))
 
 
 def medusa_paged_attention_workspace_size(kv: PagedKV, N: int, H: int) -> int:
-    return int(_lib.medusa_paged_attention_workspace_size(ctypes.byref(kv.c), int(N), int(H)))
+    return int(_lib.medusa_paged_attention_workspace_size(kv.ref, int(N), int(H)))
 
 
 def medusa_paged_attention(kv: PagedKV, layer: int, q, out, scale: float, ws, tree: Optional[Tree] = None,
@@ -770,32 +802,37 @@ def medusa_paged_attention(kv: PagedKV, layer: int, q, out, scale: float, ws, tr
     itself (N = B * tree.T)."""
     _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be [N, H, hd]")
     N, H, _ = q.shape
-    _spec("q", q, (N, H, kv.hd), kv.dtype)
-    _spec("out", out, (N, H, kv.hd), kv.dtype)
-    _chunk_starts(kv, N, chunk_starts)
+    dev = _device_of(kv.k_pages)
+    shape = (N, H, kv.hd)
+    qp = _arg("q", q, shape, kv.dtype, dev)
+    op = _arg("out", out, shape, kv.dtype, dev)
+    st = _chunk_starts(kv, N, chunk_starts, dev)
     if tree is not None:
         _require(N == kv.B * tree.T and chunk_starts is None,
                  f"with a tree q must hold {tree.T} rows per sequence, and chunk_starts be absent")
     nbytes = _nbytes("ws", ws)
-    _p(kv.k_pages)
-    _check(_lib.medusa_paged_attention(ctypes.byref(kv.c), int(layer), N, H, _p(q), float(scale),
-                                       None if tree is None else tree.handle, _p(chunk_starts), _p(out), _p(ws), nbytes,
-                                       _stream(stream)))
+    _on(kv.k_pages, dev)
+    _on(ws, dev)
+    _check(_lib.medusa_paged_attention(kv.ref, int(layer), N, H, qp, float(scale), None if tree is None else tree.handle,
+                                       st, op, ws.data_ptr(), nbytes, _stream_ptr(stream, dev)))
 
 
 def medusa_paged_accept_workspace_size(kv: PagedKV) -> int:
-    return int(_lib.medusa_paged_accept_workspace_size(ctypes.byref(kv.c)))
+    return int(_lib.medusa_paged_accept_workspace_size(kv.ref))
 
 
 def medusa_paged_accept_kv(tree: Tree, kv: PagedKV, best_path, accept_len, new_lens, ws, stream=None):
     """S7 inside the pages, every layer: the accepted rows move to the end of the prefix, and
     new_lens [B] (kv.seq_lens itself, or another buffer) receives the new lengths."""
-    for name, t in (("best_path", best_path), ("accept_len", accept_len), ("new_lens", new_lens)):
-        _spec(name, t, (kv.B,), torch.int32)
+    dev = _device_of(kv.k_pages)
+    shape = (kv.B,)
+    best = _arg("best_path", best_path, shape, torch.int32, dev)
+    acc = _arg("accept_len", accept_len, shape, torch.int32, dev)
+    new = _arg("new_lens", new_lens, shape, torch.int32, dev)
     nbytes = _nbytes("ws", ws)
-    _p(kv.k_pages)
-    _check(_lib.medusa_paged_accept_kv(tree.handle, ctypes.byref(kv.c), _p(best_path), _p(accept_len), _p(new_lens),
-                                       _p(ws), nbytes, _stream(stream)))
+    _on(kv.k_pages, dev)
+    _on(ws, dev)
+    _check(_lib.medusa_paged_accept_kv(tree.handle, kv.ref, best, acc, new, ws.data_ptr(), nbytes, _stream_ptr(stream, dev)))
 
 
 def medusa_adjust_logits(tree: Tree, logits, tree_tokens, out, history=None, history_lens=None, prompt_lens=None,
@@ -808,39 +845,41 @@ def medusa_adjust_logits(tree: Tree, logits, tree_tokens, out, history=None, his
     _require(isinstance(logits, torch.Tensor) and logits.dim() == 3, "logits must be [B, T, V]")
     B, T, V = logits.shape
     _require(T == tree.T, f"logits hold {T} tree nodes per sequence; the tree has {tree.T}")
-    _spec("logits", logits, (B, T, V), torch.float32)
-    _spec("out", out, (B, T, V), torch.float32)
+    dev = _device_of(logits)
+    i32, f32 = torch.int32, torch.float32
+    zp = _arg("logits", logits, (B, T, V), f32, dev)
+    op = _arg("out", out, (B, T, V), f32, dev)
     r = LogitRules()
-    penalties = [("repetition", repetition), ("presence", presence), ("frequency", frequency)]
-    if tree_tokens is not None or any(t is not None for _, t in penalties):
-        _spec("tree_tokens", tree_tokens, (B, T), torch.int32)
-    for name, t in penalties:
-        if t is not None:
-            _spec(name, t, (B,), torch.float32)
+    tp = None
+    if tree_tokens is not None or repetition is not None or presence is not None or frequency is not None:
+        tp = _arg("tree_tokens", tree_tokens, (B, T), i32, dev)
+    if repetition is not None:
+        r.repetition = _arg("repetition", repetition, (B,), f32, dev)
+    if presence is not None:
+        r.presence = _arg("presence", presence, (B,), f32, dev)
+    if frequency is not None:
+        r.frequency = _arg("frequency", frequency, (B,), f32, dev)
     if history is not None:
         _require(isinstance(history, torch.Tensor) and history.dim() == 2 and history.shape[1] >= 1,
                  "history must be [B, cap]")
-        _spec("history", history, (B, history.shape[1]), torch.int32)
-        _spec("history_lens", history_lens, (B,), torch.int32)
-        r.history_cap = history.shape[1]
+        cap = r.history_cap = history.shape[1]
+        r.history = _arg("history", history, (B, cap), i32, dev)
+        r.history_lens = _arg("history_lens", history_lens, (B,), i32, dev)
+        if prompt_lens is not None:
+            r.prompt_lens = _arg("prompt_lens", prompt_lens, (B,), i32, dev)
     else:
         _require(history_lens is None and prompt_lens is None, "history_lens and prompt_lens need a history")
-    if prompt_lens is not None:
-        _spec("prompt_lens", prompt_lens, (B,), torch.int32)
     _require((bias_ids is None) == (bias is None), "bias_ids and bias go together")
     if bias is not None:
         _require(isinstance(bias_ids, torch.Tensor) and bias_ids.dim() == 2 and 1 <= bias_ids.shape[1] <= MAX_BIAS,
                  f"bias_ids must be [B, n] with 1 <= n <= {MAX_BIAS}")
-        _spec("bias_ids", bias_ids, (B, bias_ids.shape[1]), torch.int32)
-        _spec("bias", bias, bias_ids.shape, torch.float32)
-        r.n_bias = bias_ids.shape[1]
+        n = r.n_bias = bias_ids.shape[1]
+        r.bias_ids = _arg("bias_ids", bias_ids, (B, n), i32, dev)
+        r.bias = _arg("bias", bias, (B, n), f32, dev)
     if allowed is not None:
-        _spec("allowed", allowed, (B, T, (V + 31) // 32), torch.int32)
-    for name, t in [("history", history), ("history_lens", history_lens), ("prompt_lens", prompt_lens),
-                    ("bias_ids", bias_ids), ("bias", bias), ("allowed", allowed)] + penalties:
-        setattr(r, name, _p(t))
-    _check(_lib.medusa_adjust_logits(tree.handle, B, V, _p(logits), _p(tree_tokens), ctypes.byref(r), _p(out),
-                                     _stream(stream)))
+        r.allowed = _arg("allowed", allowed, (B, T, (V + 31) // 32), i32, dev)
+    _on(logits, dev)
+    _check(_lib.medusa_adjust_logits(tree.handle, B, V, zp, tp, ctypes.byref(r), op, _stream_ptr(stream, dev)))
 
 
 def make_step_args(tree: Tree, t: dict, mode: int, temperature=0.0, eps=0.09, alpha=0.3,

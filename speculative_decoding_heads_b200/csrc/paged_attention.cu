@@ -60,18 +60,16 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
   __shared__ int s_last;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
   const int hd = w.kv.hd, g = w.g, hd4 = hd / 4;
-  unsigned long long begin, end;
-  int b0 = 0, h0 = 0;
-  C::template plan<NT>(w, plan, &begin, &end, &b0, &h0);
-  if (begin >= end) return;
-  const unsigned long long W = plan.before[w.kv.B];
-  unsigned long long left = end - begin;
-  Piece x = C::first_piece(w, plan, begin, b0, h0, left);
+  if (tid < 32) C::plan(w, plan);
+  __syncthreads();
+  if (plan.begin >= plan.end) return;
+  unsigned left;
+  Piece x = C::first_piece(w, plan, left);
   const int shift = w.kv.page_shift, mask = (1 << shift) - 1;
   for (;;) {
     const int b = x.b, L = plan.L[b], n = plan.n[b], first = plan.first[b];
     const int rows = min(R, n * g - x.tile * R);
-    const int keys = static_cast<int>(C::keys(w, plan, b, x.tile));
+    const int keys = C::keys(w, plan, b, x.tile);
     __syncthreads();                       // the piece before is done with shared memory
     for (int i = tid; i < R * (HD / 4); i += NT) {
       const int r = i / (HD / 4), d = i - r * (HD / 4);
@@ -189,7 +187,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
     bool write = C::whole(x);
     if (!write) {
       // Leave the piece in this CTA's slot; the last piece of the unit joins them.
-      float* slot = w.slots + C::slot(blockIdx.x, x.start, W) * slot_floats(R, HD);
+      float* slot = w.slots + C::slot(plan, blockIdx.x, x.start) * slot_floats(R, HD);
 #pragma unroll
       for (int r = 0; r < RR; ++r) {
         const int row = ty * RR + r;
@@ -204,7 +202,8 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       }
       __threadfence();
       __syncthreads();
-      const int c_lo = C::owner(x.start, W), c_hi = C::owner(x.start + x.blocks - 1, W);
+      int c_lo, c_hi;
+      C::owners(plan, x, c_lo, c_hi);
       if (tid == 0) {
         unsigned* ctr = C::counter(w, plan, x);
         s_last = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(c_hi - c_lo);
@@ -218,7 +217,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
         for (int r = 0; r < RR; ++r) {
           const int row = ty * RR + r;
           m[r] = -INFINITY;
-          for (int c = c_lo; c <= c_hi; ++c) m[r] = fmaxf(m[r], __ldcg(w.slots + C::slot(c, x.start, W) * slot_floats(R, HD) + row));
+          for (int c = c_lo; c <= c_hi; ++c) m[r] = fmaxf(m[r], __ldcg(w.slots + C::slot(plan, c, x.start) * slot_floats(R, HD) + row));
           l[r] = 0.f;
 #pragma unroll
           for (int d = 0; d < DV; ++d)
@@ -226,7 +225,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
             for (int e = 0; e < 4; ++e) o[r][d][e] = 0.f;
           const float ref = m[r] == -INFINITY ? 0.f : m[r];
           for (int c = c_lo; c <= c_hi; ++c) {
-            const float* sl = w.slots + C::slot(c, x.start, W) * slot_floats(R, HD);
+            const float* sl = w.slots + C::slot(plan, c, x.start) * slot_floats(R, HD);
             const float f = exp2f(__ldcg(sl + row) - ref);
             l[r] += f * __ldcg(sl + R + row);
 #pragma unroll

@@ -94,6 +94,25 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
+// Two fp32 operations in one instruction.
+typedef unsigned long long F2;
+__device__ __forceinline__ F2 pair(float a, float b) {
+  F2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(F2 v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
 // What every role knows of a piece.
 struct Seg {
   int n;             // key tiles of this piece
@@ -111,11 +130,14 @@ __device__ __forceinline__ Seg segment(const Params& p, const Plan& pl, const Pi
 
 using C = Cut<kBK>;
 
+// Groups of 32 keys that a tile with that many keys left has.
+__device__ __forceinline__ int tile_chunks(int keys) { return keys >= kBK ? kBK / 32 : (keys + 31) >> 5; }
+
 // ---- loads (warp 0) --------------------------------------------------------
 
 template <int HD>
 __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, const CUtensorMap* v_map, const Params& p,
-                          unsigned char* smem, Bars* bar, Piece x, unsigned long long left) {
+                          unsigned char* smem, Bars* bar, Piece x, unsigned left) {
   using S = Shape<HD>;
   const int lane = threadIdx.x & 31;
   const Plan& pl = bar->plan;
@@ -161,7 +183,7 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
   };
   for (bool ok = true; ok;) {
     const Seg s = segment(p, pl, x);
-    const int keys = static_cast<int>(C::keys(p.w, pl, x.b, x.tile));
+    const int keys = C::keys(p.w, pl, x.b, x.tile);
     int cur = lookup(x.b, x.h, x.kb0, keys), next = s.n > 1 ? lookup(x.b, x.h, x.kb0 + 1, keys) : none;
     ok = query(0, x.b, x.h, x.tile * p.w.R) && (!s.two || query(1, x.b, x.h, x.tile * p.w.R + p.rows));
     ok = ok && entry(k_map, x.kb0, cur);
@@ -190,7 +212,7 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
 // ---- products (warp 1, one thread) -----------------------------------------
 
 template <int HD>
-__device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bars* bar, Piece x, unsigned long long left) {
+__device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bars* bar, Piece x, unsigned left) {
   using S = Shape<HD>;
   constexpr uint32_t idS = tc::idesc_bf16_f32(kGroup, kBK, 0);
   constexpr uint32_t idO = tc::idesc_bf16_f32(kGroup, HD, 1);
@@ -208,23 +230,36 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
     }
     tc::mma_commit(&bar->s_full[w]);
   };
-  auto values = [&](int w, int entry, bool first) {       // O_w += P_w V
+  // O_w += P_w V over the tile's first `chunks` groups of 32 keys.  Two-group
+  // units hold P in the first half of S's columns; alternating ones hold each
+  // chunk's P and its remainder in the chunk's own 32 columns.
+  auto values = [&](int w, int entry, bool first, bool pair, int chunks) {
     if (!wait(&bar->p_full[w], np[w] & 1, bar, status)) return false;
     ++np[w];
     if (first && piece > 0 && !wait(&bar->o_free[w], (piece - 1) & 1, bar, status)) return false;
     if (!landed(entry)) return false;
     tc::fence_after_sync();
     const uint32_t vb = sbase + S::kOffRing + (entry % S::kStages) * S::kTile;
+    const uint32_t o = tmem + 256 + 128 * w, ps = tmem + 128 * w;
+    if (pair) {
+      for (int c = 0; c < chunks; ++c)
 #pragma unroll
-    for (int c = 0; c < kBK / 16; ++c)
-      tc::mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + c * 8, tc::smem_desc_sw128(vb + c * 16 * 128, S::kHalf, 1024), idO,
-                 (!first || c > 0) ? 1u : 0u);
+        for (int k = 0; k < 4; ++k)          // P and remainder, 16 keys each
+          tc::mma_ts(o, ps + 32 * c + 16 * (k & 1) + 8 * (k >> 1),
+                     tc::smem_desc_sw128(vb + (2 * c + (k >> 1)) * 16 * 128, S::kHalf, 1024), idO,
+                     (!first || c > 0 || k > 0) ? 1u : 0u);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kBK / 16; ++c)
+        tc::mma_ts(o, ps + c * 8, tc::smem_desc_sw128(vb + c * 16 * 128, S::kHalf, 1024), idO, (!first || c > 0) ? 1u : 0u);
+    }
     tc::mma_commit(&bar->pv_done[w]);
     return true;
   };
   auto release = [&](int entry) { tc::mma_commit(&bar->empty[entry % S::kStages]); };
   for (;;) {
     const Seg s = segment(p, pl, x);
+    const int keys = C::keys(p.w, pl, x.b, x.tile);
     if (!wait(&bar->q_full[0], nq[0] & 1, bar, status)) return;
     ++nq[0];
     if (s.two) {
@@ -240,13 +275,13 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
       }
       for (int i = 0; i < s.n; ++i) {
         const int v = e++;
-        if (!values(0, v, i == 0)) return;
+        if (!values(0, v, i == 0, false, 0)) return;
         if (i + 1 < s.n) {
           if (!landed(e)) return;
           scores(0, 0, e);
           if (i + 2 == s.n) tc::mma_commit(&bar->q_empty[0]);
         }
-        if (!values(1, v, i == 0)) return;
+        if (!values(1, v, i == 0, false, 0)) return;
         release(v);
         if (i + 1 < s.n) {
           scores(1, 1, e);
@@ -262,7 +297,7 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
       }
       if (s.n <= 2) tc::mma_commit(&bar->q_empty[0]);
       for (int i = 0; i < s.n; ++i) {
-        if (!values(i & 1, e, i < 2)) return;
+        if (!values(i & 1, e, i < 2, true, tile_chunks(keys - (x.kb0 + i) * kBK))) return;
         release(e++);
         if (i + 2 < s.n) {
           if (!landed(e)) return;
@@ -295,9 +330,83 @@ __device__ __forceinline__ uint64_t tree_bits(const uint64_t (&a)[4], int d) {
   return d > 0 ? ((1ull << d) - 1ull) | (a[0] << d) : anc_window(a, -d);
 }
 
+// A slot: 256 maxima, 256 sums, then O as [row / 8][column / 4][row % 8] of
+// four columns each, which a warp writes (a row per lane) and reads (eight
+// lanes per group of columns) in whole 128-byte lines.
 template <int HD>
-__device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem, Bars* bar, Piece x, unsigned long long left,
-                            unsigned long long W) {
+__device__ __forceinline__ float4* slot_out(float* slot, int row, int col4) {
+  return reinterpret_cast<float4*>(slot + 4 * kGroup) + ((row >> 3) * (HD / 4) + col4) * 8 + (row & 7);
+}
+
+// Joins the pieces that CTAs lo..hi left of a unit's row group (128 threads):
+// out = sum_y 2^(m_y - lse) O_y, lse = m + log2 sum_y 2^(m_y - m) l_y.  First a
+// thread per row finds lse; then a thread owns row thread % 8 of four blocks
+// of eight rows and every 16th group of columns, all its loads of four pieces
+// in flight together (the pieces come from L2).
+__device__ __forceinline__ float join_lse(const Work& w, const Plan& pl, unsigned start, int lo, int hi, int slot_row, int floats) {
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+  for (int y = lo; y <= hi; ++y) m = fmaxf(m, __ldcg(w.slots + static_cast<size_t>(C::slot(pl, y, start)) * floats + slot_row));
+  const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 8
+  for (int y = lo; y <= hi; ++y) {
+    const float* slot = w.slots + static_cast<size_t>(C::slot(pl, y, start)) * floats + slot_row;
+    l = fmaf(tc::ex2_ftz(__ldcg(slot) - ref), __ldcg(slot + 2 * kGroup), l);
+  }
+  return ref + __log2f(l);
+}
+
+template <int HD, typename Put>
+__device__ __forceinline__ void join(const Work& w, const Plan& pl, unsigned start, int lo, int hi, int row0, int thread,
+                                     int rows, const float* lse, Put put) {
+  constexpr int kCols = HD / 64;             // column groups per thread and row
+  const int r8 = thread & 7, c4 = thread >> 3;
+  for (int rb = 0; rb < rows; rb += 32) {
+    const int blocks = min(4, (rows - rb + 7) >> 3);
+    float4 o[4][kCols];
+    float ref[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ref[i] = i < blocks ? lse[rb + 8 * i + r8] : 0.f;
+#pragma unroll
+      for (int k = 0; k < kCols; ++k) o[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll 4
+    for (int y = lo; y <= hi; ++y) {
+      float* slot = w.slots + static_cast<size_t>(C::slot(pl, y, start)) * slot_floats(2 * kGroup, HD);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = row0 + rb + 8 * i + r8;
+        float f = 0.f;
+        float4 v4[kCols];
+        if (i < blocks) {
+          f = tc::ex2_ftz(__ldcg(slot + row) - ref[i]);
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) v4[k] = __ldcg(slot_out<HD>(slot, row, c4 + 16 * k));
+        } else {
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) v4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) {
+          const float4 v = v4[k];
+          o[i][k].x = fmaf(f, v.x, o[i][k].x);
+          o[i][k].y = fmaf(f, v.y, o[i][k].y);
+          o[i][k].z = fmaf(f, v.z, o[i][k].z);
+          o[i][k].w = fmaf(f, v.w, o[i][k].w);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < blocks)
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) put(rb + 8 * i + r8, 4 * (c4 + 16 * k), o[i][k].x, o[i][k].y, o[i][k].z, o[i][k].w);
+  }
+}
+
+template <int HD>
+__device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem, Bars* bar, Piece x, unsigned left) {
   using S = Shape<HD>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = (warp - 4) >> 2;             // softmax warpgroup
@@ -312,6 +421,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
   int entries = 0;                           // ring entries before this piece
   int syncs = 0;                             // uses of this warpgroup's barrier
   int singles = 0;                           // alternating pieces before this one
+  int piece = 0;                             // pieces before this one
   for (;;) {
     const Seg s = segment(p, pl, x);
     const int b = x.b, L = pl.L[b], n = pl.n[b];
@@ -319,7 +429,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
     const int rows = s.two ? (w == 0 ? p.rows : s.rows - p.rows) : s.rows;
     const bool active = 32 * quarter < rows; // a warp without rows only keeps the barriers going
     const int tok = (grp_row + row) / p.w.g;
-    const int keys = static_cast<int>(C::keys(p.w, pl, b, x.tile));
+    const int keys = C::keys(p.w, pl, b, x.tile);
     const bool tree = p.w.t.T > 0;
     uint64_t anc[4] = {0ull, 0ull, 0ull, 0ull};
     if (tree && row < rows) {
@@ -341,21 +451,24 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         for (int c = 0; c < kBK; c += 32) tc::tmem_ld32(tS + c, sv + c);
         tc::tmem_wait_ld();
         if (j0 + kBK > clear) {
-          if (tree) {
-            const uint64_t a = tree_bits(anc, L - j0), c = tree_bits(anc, L - j0 - 64);
-            const uint32_t bits[4] = {static_cast<uint32_t>(a), static_cast<uint32_t>(a >> 32), static_cast<uint32_t>(c),
-                                      static_cast<uint32_t>(c >> 32)};
+          uint32_t bits[4];
 #pragma unroll
-            for (int k = 0; k < kBK; ++k) sv[k] = ((bits[k >> 5] >> (k & 31)) & 1u) ? sv[k] : -INFINITY;
-          } else {
-            const int lim = limit - j0;
-#pragma unroll
-            for (int k = 0; k < kBK; ++k) sv[k] = k < lim ? sv[k] : -INFINITY;
+          for (int c = 0; c < 4; ++c) {
+            if (tree) {
+              bits[c] = static_cast<uint32_t>(tree_bits(anc, L - j0 - 32 * c));
+            } else {
+              const int lim = limit - j0 - 32 * c;
+              bits[c] = lim >= 32 ? ~0u : lim <= 0 ? 0u : (1u << lim) - 1u;
+            }
           }
-        }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < kBK; ++k) mx[k & 3] = fmaxf(mx[k & 3], sv[k]);
+          for (int k = 0; k < kBK; ++k) sv[k] = (bits[k >> 5] >> (k & 31)) & 1u ? sv[k] : -INFINITY;
+        }
+        float mx[4] = {sv[0], sv[1], sv[2], sv[3]};
+#pragma unroll
+        for (int k = 4; k < kBK; k += 8)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) mx[u] = fmaxf(mx[u], k + 4 < kBK ? fmaxf(sv[k + u], sv[k + 4 + u]) : sv[k + u]);
         const float tm = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
         float factor = 1.f;
         if (tm > m + kRescaleLog2 || (m == -INFINITY && tm > -INFINITY)) {
@@ -363,9 +476,8 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           m = tm;
         }
         const float ref = m == -INFINITY ? 0.f : -m;
-        const bool first = s.two ? i == 0 : i < 2;
         // O is rescaled before P is handed over; P V of the step before is done (S was issued after it).
-        if (!first && __any_sync(0xffffffffu, factor != 1.f)) {
+        if (i >= (s.two ? 1 : 2) && __any_sync(0xffffffffu, factor != 1.f)) {
 #pragma unroll 1
           for (int c = 0; c < HD; c += 32) {
             float o[32];
@@ -376,20 +488,36 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
             tc::tmem_st32(tmem + lanes + 256 + 128 * w + c, o);
           }
         }
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const F2 sc = pair(p.scale_log2, p.scale_log2), rf = pair(ref, ref);
+        F2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < kBK; c += 32) {
-          uint32_t pk[16];
+        for (int c = 0; c < kBK / 32; ++c) {
+          uint32_t hi[16];
+          float pv0[32];
 #pragma unroll
           for (int k = 0; k < 32; k += 2) {
-            const float a = tc::ex2_ftz(fmaf(sv[c + k], p.scale_log2, ref)), d = tc::ex2_ftz(fmaf(sv[c + k + 1], p.scale_log2, ref));
-            sum[k & 2] += a;
-            sum[(k & 2) + 1] += d;
-            pk[k / 2] = pack2(a, d);
+            float a, d;
+            unpair(fma2(pair(sv[32 * c + k], sv[32 * c + k + 1]), sc, rf), a, d);
+            a = tc::ex2_ftz(a);
+            d = tc::ex2_ftz(d);
+            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(a, d));
+            hi[k / 2] = pack2(a, d);
+            pv0[k] = a;
+            pv0[k + 1] = d;
           }
-          tc::tmem_st16(tS + c / 2, pk);
+          if (s.two) {
+            tc::tmem_st16(tS + 16 * c, hi);
+          } else {
+            uint32_t lo[16];                 // the remainder of P
+#pragma unroll
+            for (int k = 0; k < 16; ++k) lo[k] = pack2(pv0[2 * k] - bf16lo(hi[k]), pv0[2 * k + 1] - bf16hi(hi[k]));
+            tc::tmem_st16(tS + 32 * c, hi);
+            tc::tmem_st16(tS + 32 * c + 16, lo);
+          }
         }
-        l = l * factor + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+        float s0, s1;
+        unpair(add2(sum[0], sum[1]), s0, s1);
+        l = l * factor + (s0 + s1);
         tc::tmem_wait_st();
       }
       if ((w == 0 || !s.two) && x.kb0 + i == x.blocks - 1 && (keys & (p.box - 1)) != 0) {
@@ -417,15 +545,14 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
     float f0 = 1.f, f1 = 0.f;
     if (!s.two) {
       if (w == 1) {
-        // the statistics before these have been read
-        if (singles > 0 && !wait(&bar->stat_free, (singles - 1) & 1, bar, status)) return;
+        // the first warpgroup is done with the piece before
+        if (piece > 0 && !wait(&bar->stat_free, (piece - 1) & 1, bar, status)) return;
         bar->m1[row] = m;
         bar->l1[row] = l;
         tc::mbar_arrive(&bar->stat_full);
       } else {
         if (!wait(&bar->stat_full, singles & 1, bar, status)) return;
         const float m1 = bar->m1[row], l1 = bar->l1[row], mm = fmaxf(m, m1);
-        tc::mbar_arrive(&bar->stat_free);
         f0 = m == -INFINITY ? 0.f : tc::ex2_ftz(m - mm);
         f1 = m1 == -INFINITY ? 0.f : tc::ex2_ftz(m1 - mm);
         m = mm;
@@ -440,16 +567,15 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
       tc::fence_after_sync();
       const bool whole = C::whole(x);
       const int slot_row = (s.two ? w * kGroup : 0) + row;           // rows of a slot: 2 * kGroup
-      float* slot = p.w.slots + C::slot(blockIdx.x, x.start, W) * slot_floats(2 * kGroup, HD);
+      float* slot = p.w.slots + C::slot(pl, blockIdx.x, x.start) * slot_floats(2 * kGroup, HD);
       uint16_t* dst = p.out + (static_cast<size_t>(pl.first[b] + tok) * p.w.H + x.h * p.w.g + (grp_row + row - tok * p.w.g)) * HD;
       const float inv = 1.f / l;
-      auto put = [&](int c, const float (&o)[32], float by) {
-        if (row >= rows) return;
-#pragma unroll
-        for (int k = 0; k < 32; k += 8)
-          *reinterpret_cast<uint4*>(dst + c + k) =
-              make_uint4(pack2(o[k] * by, o[k + 1] * by), pack2(o[k + 2] * by, o[k + 3] * by),
-                         pack2(o[k + 4] * by, o[k + 5] * by), pack2(o[k + 6] * by, o[k + 7] * by));
+      // Columns c .. c + 3 of row r of the group.
+      auto put = [&](int r, int c, float a, float d, float e, float f) {
+        if (r >= rows) return;
+        const int t = (grp_row + r) / p.w.g;
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(pl.first[b] + t) * p.w.H + x.h * p.w.g + (grp_row + r - t * p.w.g)) * HD + c) =
+            make_uint2(pack2(a, d), pack2(e, f));
       };
       if (active) {
 #pragma unroll 1
@@ -465,11 +591,16 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
             for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], f1, o[k] * f0);
           }
           if (whole) {
-            put(c, o, inv);
-          } else {
-            float4* d = reinterpret_cast<float4*>(slot + 4 * kGroup) + (c / 4) * (2 * kGroup) + slot_row;
+            if (row < rows)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) __stcg(d + k * (2 * kGroup), make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
+              for (int k = 0; k < 32; k += 8)
+                *reinterpret_cast<uint4*>(dst + c + k) =
+                    make_uint4(pack2(o[k] * inv, o[k + 1] * inv), pack2(o[k + 2] * inv, o[k + 3] * inv),
+                               pack2(o[k + 4] * inv, o[k + 5] * inv), pack2(o[k + 6] * inv, o[k + 7] * inv));
+          } else {
+            float4* d = slot_out<HD>(slot, slot_row, c / 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) __stcg(d + 8 * k, make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]));
           }
         }
       }
@@ -487,7 +618,8 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         __threadfence();
         tc::mbar_arrive(&bar->group[w]);
         if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
-        const int lo = C::owner(x.start, W), hi = C::owner(x.start + x.blocks - 1, W);
+        int lo, hi;
+        C::owners(pl, x, lo, hi);
         if (row == 0) {
           unsigned* ctr = C::counter(p.w, pl, x) + w;
           bar->last[w] = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(hi - lo);
@@ -495,37 +627,23 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         }
         tc::mbar_arrive(&bar->group[w]);
         if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
-        if (bar->last[w] && active) {
+        if (bar->last[w]) {
           __threadfence();
-          auto at = [&](int c) { return p.w.slots + C::slot(c, x.start, W) * slot_floats(2 * kGroup, HD); };
-          float mm = -INFINITY, ll = 0.f;
-          for (int c = lo; c <= hi; ++c) mm = fmaxf(mm, __ldcg(at(c) + slot_row));
-          const float ref = mm == -INFINITY ? 0.f : mm;
-          for (int c = lo; c <= hi; ++c) ll += tc::ex2_ftz(__ldcg(at(c) + slot_row) - ref) * __ldcg(at(c) + 2 * kGroup + slot_row);
-#pragma unroll 1
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = 0.f;
-            for (int y = lo; y <= hi; ++y) {
-              const float f = tc::ex2_ftz(__ldcg(at(y) + slot_row) - ref);
-              const float4* d = reinterpret_cast<const float4*>(at(y) + 4 * kGroup) + (c / 4) * (2 * kGroup) + slot_row;
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const float4 v = __ldcg(d + k * (2 * kGroup));
-                o[4 * k] = fmaf(f, v.x, o[4 * k]);
-                o[4 * k + 1] = fmaf(f, v.y, o[4 * k + 1]);
-                o[4 * k + 2] = fmaf(f, v.z, o[4 * k + 2]);
-                o[4 * k + 3] = fmaf(f, v.w, o[4 * k + 3]);
-              }
-            }
-            put(c, o, 1.f / ll);
-          }
+          // The hand-over arrays hold the rows' lse: the first's maxima are its
+          // own until it frees them, the second waits for that.
+          float* lse = w == 0 ? bar->m1 : bar->l1;
+          if (w == 1 && piece > 0 && !wait(&bar->stat_free, (piece - 1) & 1, bar, status)) return;
+          lse[row] = row < rows ? join_lse(p.w, pl, x.start, lo, hi, slot_row, static_cast<int>(slot_floats(2 * kGroup, HD))) : 0.f;
+          tc::mbar_arrive(&bar->group[w]);
+          if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
+          join<HD>(p.w, pl, x.start, lo, hi, s.two ? w * kGroup : 0, row, rows, lse, put);
         }
       }
     }
+    if (w == 0) tc::mbar_arrive(&bar->stat_free);
     pv[0] += n0;
     pv[1] += n1;
+    ++piece;
     if (left == 0) return;
     C::next_piece(p.w, pl, x, left);
   }
@@ -543,55 +661,73 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   Bars* bar = reinterpret_cast<Bars*>(smem + S::kOffBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  if (tid == 0) {
-    for (int st = 0; st < S::kStages; ++st) {
-      mbar_init(&bar->full[st], 1);
-      mbar_init(&bar->empty[st], 1);
+  // Registers: launched with 168 a thread; the softmax warpgroups take what the others give up
+  // (128 * 104 + 256 * 200 = 384 * 168).
+  if (warp == 0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (lane == 0) {
+      for (int st = 0; st < S::kStages; ++st) {
+        mbar_init(&bar->full[st], 1);
+        mbar_init(&bar->empty[st], 1);
+      }
+      for (int w = 0; w < 2; ++w) {
+        mbar_init(&bar->q_full[w], 1);
+        mbar_init(&bar->q_empty[w], 1);
+        mbar_init(&bar->s_full[w], 1);
+        mbar_init(&bar->p_full[w], 4);
+        mbar_init(&bar->pv_done[w], 1);
+        mbar_init(&bar->o_free[w], 4);
+        mbar_init(&bar->group[w], kGroup);
+      }
+      mbar_init(&bar->stat_full, kGroup);
+      mbar_init(&bar->stat_free, kGroup);
+      bar->abort = 0;
+      fence_barrier_init();
     }
-    for (int w = 0; w < 2; ++w) {
-      mbar_init(&bar->q_full[w], 1);
-      mbar_init(&bar->q_empty[w], 1);
-      mbar_init(&bar->s_full[w], 1);
-      mbar_init(&bar->p_full[w], 4);
-      mbar_init(&bar->pv_done[w], 1);
-      mbar_init(&bar->o_free[w], 4);
-      mbar_init(&bar->group[w], kGroup);
-    }
-    mbar_init(&bar->stat_full, kGroup);
-    mbar_init(&bar->stat_free, kGroup);
-    bar->abort = 0;
-    fence_barrier_init();
-    tc::prefetch_tensormap(&q_map);
-    tc::prefetch_tensormap(&k_map);
-    tc::prefetch_tensormap(&v_map);
-  }
-  if (warp == 1) {
-    tc::tmem_alloc(&bar->tmem_base, kTmemCols);
-    tc::tmem_relinquish();
-  }
-  unsigned long long begin, end;
-  int b0 = 0, h0 = 0;
-  C::plan<kThreads>(p.w, bar->plan, &begin, &end, &b0, &h0);
-  tc::fence_before_sync();
-  __syncthreads();
-  tc::fence_after_sync();
-  const uint32_t tmem = bar->tmem_base;
-  if (begin < end) {
-    unsigned long long left = end - begin;
-    const Piece x = C::first_piece(p.w, bar->plan, begin, b0, h0, left);
-    if (warp == 0) {
+    __syncwarp();
+    C::plan(p.w, bar->plan);
+    __syncwarp();
+    // The loads need nothing of the other warps: they start here.
+    __threadfence_block();
+    asm volatile("barrier.cta.arrive 1, 384;" ::: "memory");
+    if (bar->plan.begin < bar->plan.end) {
+      unsigned left;
+      const Piece x = C::first_piece(p.w, bar->plan, left);
       run_loads<HD>(&q_map, &k_map, &v_map, p, smem, bar, x, left);
-    } else if (warp == 1) {
-      if (lane == 0) run_products<HD>(p, smem_u32(smem), tmem, bar, x, left);
-    } else if (warp >= 4) {
-      run_softmax<HD>(p, smem, tmem, bar, x, left, bar->plan.before[p.w.kv.B]);
+    }
+  } else if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 1) {
+      tc::tmem_alloc(&bar->tmem_base, kTmemCols);
+      tc::tmem_relinquish();
+    } else if (tid == 64) {
+      tc::prefetch_tensormap(&q_map);
+      tc::prefetch_tensormap(&k_map);
+      tc::prefetch_tensormap(&v_map);
+    }
+    tc::fence_before_sync();
+    asm volatile("barrier.cta.sync 1, 384;" ::: "memory");
+    tc::fence_after_sync();
+    if (tid == 32 && bar->plan.begin < bar->plan.end) {
+      unsigned left;
+      const Piece x = C::first_piece(p.w, bar->plan, left);
+      run_products<HD>(p, smem_u32(smem), bar->tmem_base, bar, x, left);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    asm volatile("barrier.cta.sync 1, 384;" ::: "memory");
+    tc::fence_after_sync();
+    if (bar->plan.begin < bar->plan.end) {
+      unsigned left;
+      const Piece x = C::first_piece(p.w, bar->plan, left);
+      run_softmax<HD>(p, smem, bar->tmem_base, bar, x, left);
     }
   }
   tc::fence_before_sync();
   __syncthreads();
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, kTmemCols);
+    tc::tmem_dealloc(bar->tmem_base, kTmemCols);
   }
 }
 

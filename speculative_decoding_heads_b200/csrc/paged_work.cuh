@@ -8,8 +8,19 @@
 // (the lengths are device memory).  A unit that a range boundary cuts is
 // computed in pieces: each piece leaves its unnormalised output, row maxima
 // and row sums in the CTA's slot, and the piece that finishes last (a counter
-// per unit) joins them in range order, so the result does not depend on who
-// was last.
+// per unit and row group) joins them in range order, so the result does not
+// depend on who was last.
+//
+// Where every sequence is one tile and there are fewer units than CTAs (a few
+// requests decoding), a cut at unit boundaries is better: every unit gets a
+// whole number of CTAs, at most `each` blocks to each, and no CTA pays for two
+// pieces.  It is taken when it costs a CTA at most two blocks more than the
+// equal cut (the set-up and output of a second piece take about as long).
+//
+// One warp lays the plan, two sequences to a lane: the blocks of a sequence's
+// first t tiles, sum_{i=1..t} ceil((g L + i R) / (g BK)), have a closed form
+// (the floor sum of an arithmetic progression, by the Euclidean descent of
+// its slope), so neither the total nor a CTA's start needs a walk over tiles.
 #pragma once
 
 #include "common.cuh"
@@ -32,170 +43,234 @@ struct Work {
 
 struct Plan {
   int L[MEDUSA_MAX_B], n[MEDUSA_MAX_B], first[MEDUSA_MAX_B];
-  int tile0[MEDUSA_MAX_B + 1];                  // tiles of the sequences before
-  unsigned long long before[MEDUSA_MAX_B + 1];  // key blocks of the sequences before, all heads
-  unsigned long long scan[12];
-  int tile, block;                              // where this CTA starts
+  int tile0[MEDUSA_MAX_B + 1];         // tiles of the sequences before
+  unsigned total;                      // W: key blocks of all units
+  unsigned each;                       // cut at unit boundaries: blocks per CTA; 0: equal ranges
+  unsigned begin, end;                 // this CTA's range
+  int b, h, tile, block;               // where it starts
+  int lo, hi;                          // cut at unit boundaries: the CTAs of its unit
 };
 
 // A run of key blocks of one unit.
 struct Piece {
   int b, h, tile;
   int kb0, kb1, blocks;        // [kb0, kb1) of the unit's blocks
-  unsigned long long start;    // offset of the unit in the whole list
+  unsigned start;              // offset of the unit in the whole list
 };
+
+// sum_{i=0}^{n-1} floor((a i + b) / m)
+__device__ __forceinline__ unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a,
+                                                        unsigned long long b) {
+  unsigned long long s = 0;
+  while (n > 0) {
+    if (a >= m) {
+      s += n * (n - 1) / 2 * (a / m);
+      a %= m;
+    }
+    if (b >= m) {
+      s += n * (b / m);
+      b %= m;
+    }
+    const unsigned long long y = a * n + b;   // the line's height: count its lattice points from the other axis
+    if (y < m) break;
+    n = y / m;
+    b = y % m;
+    const unsigned long long t = m;
+    m = a;
+    a = t;
+  }
+  return s;
+}
 
 template <int BK>
 struct Cut {
-  static __device__ __forceinline__ int tiles(const Work& w, int n) {
-    return static_cast<int>((static_cast<long long>(n) * w.g + w.R - 1) / w.R);
-  }
   // Rows of the cache that the tile's last row can see.
-  static __device__ __forceinline__ long long keys(const Work& w, const Plan& p, int b, int tile) {
+  static __device__ __forceinline__ int keys(const Work& w, const Plan& p, int b, int tile) {
     const int n = p.n[b];
-    if (w.t.T > 0) return static_cast<long long>(p.L[b]) + n;
-    const int last = static_cast<int>((static_cast<long long>(tile + 1) * w.R - 1) / w.g) + 1;
-    return static_cast<long long>(p.L[b]) + (last < n ? last : n);
+    if (w.t.T > 0) return p.L[b] + n;
+    const int last = ((tile + 1) * w.R - 1) / w.g + 1;
+    return p.L[b] + (last < n ? last : n);
   }
   static __device__ __forceinline__ int blocks(const Work& w, const Plan& p, int b, int tile) {
-    return static_cast<int>((keys(w, p, b, tile) + BK - 1) / BK);
+    return (keys(w, p, b, tile) + BK - 1) / BK;
+  }
+  // Blocks of the first t tiles of one head.
+  static __device__ __forceinline__ unsigned long long before_tile(const Work& w, int L, int n, int tiles, int t) {
+    const unsigned long long all = (static_cast<unsigned>(L) + n + BK - 1) / BK;
+    if (t == 0) return 0ull;
+    if (w.t.T > 0) return all * t;
+    const unsigned long long m = static_cast<unsigned long long>(w.g) * BK;
+    const int k = t < tiles ? t : tiles - 1;     // the last tile ends with the chunk
+    const unsigned long long s =
+        k == 0 ? 0ull : floor_sum(k, m, w.R, static_cast<unsigned long long>(w.g) * L + w.R + m - 1);
+    return t < tiles ? s : s + all;
   }
 
-  // Every thread of the CTA; returns this CTA's range [begin, end) of the list
-  // and sets p.tile / p.block and *b, *h to its start.
-  template <int kThreads>
-  static __device__ void plan(const Work& w, Plan& p, unsigned long long* begin, unsigned long long* end, int* b_out,
-                              int* h_out) {
-    const int tid = threadIdx.x, lane = tid & 31, B = w.kv.B;
-    if (tid < MEDUSA_MAX_B) {
-      int L = 0, n = 0, first = 0;
-      if (tid < B) {
-        L = w.kv.lens[tid];
+  // One whole warp; the other threads see the plan after the next __syncthreads.
+  static __device__ void plan(const Work& w, Plan& p) {
+    const int lane = threadIdx.x & 31, B = w.kv.B;
+    const unsigned hk = w.kv.Hkv;
+    int L[2], n[2], tiles[2];
+    unsigned long long work[2];
+    const long long cap = static_cast<long long>(w.kv.max_pages) << w.kv.page_shift;
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int b = 2 * lane + i;
+      int first = 0;
+      L[i] = n[i] = 0;
+      if (b < B) {
+        L[i] = w.kv.lens[b];
         if (w.starts) {
-          first = w.starts[tid];
-          n = w.starts[tid + 1] - first;
+          first = w.starts[b];
+          n[i] = w.starts[b + 1] - first;
         } else {
-          n = w.N / B;
-          first = n * tid;
+          n[i] = w.N / B;
+          first = n[i] * b;
         }
-        const long long cap = static_cast<long long>(w.kv.max_pages) << w.kv.page_shift;
-        const bool ok = n == 0 || (n > 0 && first >= 0 && first <= w.N - n && L >= 0 && static_cast<long long>(L) + n <= cap &&
-                                   static_cast<long long>(L) + n < 0x7fffff00ll);
+        const bool ok = n[i] == 0 || (n[i] > 0 && first >= 0 && first <= w.N - n[i] && L[i] >= 0 &&
+                                      static_cast<long long>(L[i]) + n[i] <= cap &&
+                                      static_cast<long long>(L[i]) + n[i] < 0x7fffff00ll);
         if (!ok) {
-          n = 0;
-          if (blockIdx.x == 0) set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
+          n[i] = 0;
+          bad = true;
         }
       }
-      p.L[tid] = L;
-      p.n[tid] = n;
-      p.first[tid] = first;
-      p.before[tid + 1] = 0ull;              // first: key blocks of one head of the sequence
+      p.L[b] = L[i];
+      p.n[b] = n[i];
+      p.first[b] = first;
+      tiles[i] = (n[i] * w.g + w.R - 1) / w.R;
+      work[i] = n[i] > 0 ? before_tile(w, L[i], n[i], tiles[i], tiles[i]) * hk : 0ull;
     }
-    __syncthreads();
-    if (tid < 32) {
-      const int x = tiles(w, p.n[2 * lane]), y = tiles(w, p.n[2 * lane + 1]);
-      int s = x + y;
-      for (int o = 1; o < 32; o <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += v;
+    // Tiles (below 2^23) and blocks, summed over the lanes before in one word.
+    unsigned long long both = (work[0] + work[1]) << 23 | static_cast<unsigned>(tiles[0] + tiles[1]);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned long long v = __shfl_up_sync(0xffffffffu, both, o);
+      if (lane >= o) both += v;
+    }
+    const unsigned long long ws = both >> 23;
+    const int ts = static_cast<int>(both & 0x7fffffu);
+    p.tile0[2 * lane + 1] = ts - tiles[1];
+    p.tile0[2 * lane + 2] = ts;
+    if (lane == 0) p.tile0[0] = 0;
+    both = __shfl_sync(0xffffffffu, both, 31);
+    unsigned long long W = both >> 23;
+    if (W > 0x7fffffffull) {     // 2^31 blocks of keys in one call: refused like any other impossible chunk
+      W = 0;
+      bad = true;
+    }
+    if (bad && blockIdx.x == 0) set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
+    const unsigned c = blockIdx.x, C = gridDim.x, units = static_cast<unsigned>(both & 0x7fffffu) * hk;
+    if (W > 0 && units < C && __all_sync(0xffffffffu, tiles[0] <= 1 && tiles[1] <= 1)) {
+      // sum_u ceil(blocks_u / each) <= W / each + units <= C
+      const unsigned total = static_cast<unsigned>(W), each = (total + C - units - 1) / (C - units);
+      if (each <= total / C + 2) {
+        if (lane == 0) {
+          p.total = total;
+          p.each = each;
+          p.begin = p.end = 0;
+        }
+        __syncwarp();
+        unsigned cnt[2], blk[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          blk[i] = static_cast<unsigned>(work[i]) / hk;
+          cnt[i] = (blk[i] + each - 1) / each;            // CTAs of one unit
+        }
+        unsigned at = (cnt[0] + cnt[1]) * hk;             // CTAs before the next lane's sequences
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned v = __shfl_up_sync(0xffffffffu, at, o);
+          if (lane >= o) at += v;
+        }
+        at -= (cnt[0] + cnt[1]) * hk;
+        const int i = c >= at + cnt[0] * hk ? 1 : 0;
+        if (i) at += cnt[0] * hk;
+        const unsigned k = i ? cnt[1] : cnt[0], nb = i ? blk[1] : blk[0];
+        if (c >= at && c < at + k * hk) {
+          const unsigned h = (c - at) / k, part = c - at - h * k;
+          p.b = 2 * lane + i;
+          p.h = static_cast<int>(h);
+          p.tile = 0;
+          p.block = static_cast<int>(nb * part / k);
+          p.end = nb * (part + 1) / k - p.block;
+          p.lo = static_cast<int>(at + h * k);
+          p.hi = static_cast<int>(at + h * k + k - 1);
+        }
+        return;
       }
-      p.tile0[2 * lane + 1] = s - y;
-      p.tile0[2 * lane + 2] = s;
-      if (lane == 0) p.tile0[0] = 0;
     }
-    __syncthreads();
-    const int total_tiles = p.tile0[B];
-    for (int t = tid; t < total_tiles; t += kThreads) {
-      int lo = 0, hi = B;                    // largest b with tile0[b] <= t
+    const unsigned r = ranges(static_cast<unsigned>(W));
+    const unsigned begin = c < r ? range_begin(c, static_cast<unsigned>(W)) : 0u;
+    const unsigned end = c < r ? range_begin(c + 1, static_cast<unsigned>(W)) : 0u;
+    if (lane == 0) {
+      p.total = static_cast<unsigned>(W);
+      p.each = 0u;
+      p.begin = begin;
+      p.end = end;
+    }
+    if (begin >= end) return;
+    // The lane whose sequences hold offset begin, and where in them it lies.
+    unsigned long long off = ws - work[0] - work[1];      // blocks before this lane's sequences
+    const bool mine = begin >= off && begin < ws;
+    if (mine) {
+      const int i = begin >= off + work[0] ? 1 : 0;
+      if (i) off += work[0];
+      const unsigned rem = begin - static_cast<unsigned>(off), per_head = static_cast<unsigned>(i ? work[1] : work[0]) / hk;
+      const int h = rem / per_head;
+      const unsigned at = rem - h * per_head;
+      const int Li = i ? L[1] : L[0], ni = i ? n[1] : n[0], nt = i ? tiles[1] : tiles[0];
+      int lo = 0, hi = nt;                                // largest tile with before_tile(tile) <= at
+      unsigned long long at_lo = 0ull;
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.tile0[mid] <= t) lo = mid; else hi = mid;
+        const unsigned long long s = before_tile(w, Li, ni, nt, mid);
+        if (s <= at) {
+          lo = mid;
+          at_lo = s;
+        } else {
+          hi = mid;
+        }
       }
-      atomicAdd(&p.before[lo + 1], static_cast<unsigned long long>(blocks(w, p, lo, t - p.tile0[lo])));
+      p.b = 2 * lane + i;
+      p.h = h;
+      p.tile = lo;
+      p.block = static_cast<int>(at - static_cast<unsigned>(at_lo));
     }
-    __syncthreads();
-    if (tid < 32) {
-      const unsigned long long hk = w.kv.Hkv;
-      const unsigned long long x = p.before[2 * lane + 1] * hk, y = p.before[2 * lane + 2] * hk;
-      unsigned long long s = x + y;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long v = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += v;
-      }
-      p.before[2 * lane + 1] = s - y;
-      p.before[2 * lane + 2] = s;
-      if (lane == 0) p.before[0] = 0ull;
-    }
-    __syncthreads();
-    // No more ranges than blocks, so that none is empty.
-    const unsigned long long W = p.before[B], C = ranges(W), c = blockIdx.x;
-    *begin = *end = 0ull;
-    if (c >= C) return;
-    *begin = W * c / C;
-    *end = W * (c + 1) / C;
-    int lo = 0, hi = B;                      // largest b with before[b] <= begin (empty sequences in between skip ahead)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.before[mid] <= *begin) lo = mid; else hi = mid;
-    }
-    unsigned long long rem = *begin - p.before[lo];
-    const unsigned long long per_head = (p.before[lo + 1] - p.before[lo]) / w.kv.Hkv;
-    *b_out = lo;
-    *h_out = static_cast<int>(rem / per_head);
-    rem -= *h_out * per_head;
-    const int nt = p.tile0[lo + 1] - p.tile0[lo];
-    if (nt == 1) {
-      if (tid == 0) {
-        p.tile = 0;
-        p.block = static_cast<int>(rem);
-      }
-      __syncthreads();
-      return;
-    }
-    // The tile of that head whose blocks hold offset rem.
-    unsigned long long acc = 0ull;
-    for (int t0 = 0; t0 < nt; t0 += kThreads) {
-      const int t = t0 + tid;
-      const unsigned long long mine = t < nt ? blocks(w, p, lo, t) : 0;
-      unsigned long long s = mine;
-      for (int o = 1; o < 32; o <<= 1) {
-        const unsigned long long v = __shfl_up_sync(0xffffffffu, s, o);
-        if (lane >= o) s += v;
-      }
-      if (lane == 31) p.scan[tid >> 5] = s;
-      __syncthreads();
-      unsigned long long off = acc, all = acc;
-      for (int k = 0; k < kThreads / 32; ++k) {
-        if (k < (tid >> 5)) off += p.scan[k];
-        all += p.scan[k];
-      }
-      s += off;
-      if (mine > 0 && rem >= s - mine && rem < s) {
-        p.tile = t;
-        p.block = static_cast<int>(rem - (s - mine));
-      }
-      __syncthreads();
-      acc = all;
-      if (acc > rem) break;
-    }
-    __syncthreads();
+  }
+
+  // No more ranges than blocks, so that none is empty; the first W mod C hold one block more.
+  static __device__ __forceinline__ unsigned ranges(unsigned W) { return W < gridDim.x ? W : gridDim.x; }
+  static __device__ __forceinline__ unsigned range_begin(unsigned c, unsigned W) {
+    const unsigned C = ranges(W), each = W / C, more = W - each * C;
+    return each * c + (c < more ? c : more);
+  }
+  // The CTAs that hold a piece's unit.
+  static __device__ __forceinline__ void owners(const Plan& p, const Piece& x, int& lo, int& hi) {
+    lo = p.each ? p.lo : owner(x.start, p.total);
+    hi = p.each ? p.hi : owner(x.start + x.blocks - 1, p.total);
+  }
+  static __device__ __forceinline__ int owner(unsigned off, unsigned W) {
+    const unsigned C = ranges(W), each = W / C, more = W - each * C;
+    return off < more * (each + 1) ? off / (each + 1) : more + (off - more * (each + 1)) / each;
   }
 
   // The first piece of a CTA's range, and the one after `x`; `left` counts the
   // range's blocks that no piece has taken yet (0: there is none).
-  static __device__ __forceinline__ Piece first_piece(const Work& w, const Plan& p, unsigned long long begin, int b, int h,
-                                                      unsigned long long& left) {
+  static __device__ __forceinline__ Piece first_piece(const Work& w, const Plan& p, unsigned& left) {
     Piece x;
-    x.b = b;
-    x.h = h;
+    left = p.end - p.begin;
+    x.b = p.b;
+    x.h = p.h;
     x.tile = p.tile;
     x.kb0 = p.block;
-    x.start = begin - p.block;
-    x.blocks = blocks(w, p, b, x.tile);
+    x.start = p.begin - p.block;
+    x.blocks = blocks(w, p, x.b, x.tile);
     take(x, left);
     return x;
   }
-  static __device__ __forceinline__ void next_piece(const Work& w, const Plan& p, Piece& x, unsigned long long& left) {
+  static __device__ __forceinline__ void next_piece(const Work& w, const Plan& p, Piece& x, unsigned& left) {
     x.start += x.blocks;
     x.kb0 = 0;
     if (++x.tile == p.tile0[x.b + 1] - p.tile0[x.b]) {
@@ -208,27 +283,21 @@ struct Cut {
     x.blocks = blocks(w, p, x.b, x.tile);
     take(x, left);
   }
-  static __device__ __forceinline__ void take(Piece& x, unsigned long long& left) {
-    const unsigned long long room = static_cast<unsigned long long>(x.blocks - x.kb0);
-    const int m = static_cast<int>(room < left ? room : left);
-    x.kb1 = x.kb0 + m;
+  static __device__ __forceinline__ void take(Piece& x, unsigned& left) {
+    const unsigned room = static_cast<unsigned>(x.blocks - x.kb0);
+    const unsigned m = room < left ? room : left;
+    x.kb1 = x.kb0 + static_cast<int>(m);
     left -= m;
   }
   static __device__ __forceinline__ bool whole(const Piece& x) { return x.kb0 == 0 && x.kb1 == x.blocks; }
 
-  static __device__ __forceinline__ unsigned long long ranges(unsigned long long W) {
-    return W < gridDim.x ? W : gridDim.x;
-  }
-  // The CTA whose range holds an offset of the list.
-  static __device__ __forceinline__ int owner(unsigned long long off, unsigned long long W) {
-    return static_cast<int>(((off + 1) * ranges(W) - 1) / W);
-  }
   static __device__ __forceinline__ unsigned* counter(const Work& w, const Plan& p, const Piece& x) {
     return w.counters + (static_cast<size_t>(p.tile0[x.b] + x.tile) * w.kv.Hkv + x.h) * kCounters;
   }
-  // Which of CTA c's two slots holds its piece of the unit starting at `start`.
-  static __device__ __forceinline__ int slot(int c, unsigned long long start, unsigned long long W) {
-    return 2 * c + (start < W * static_cast<unsigned long long>(c) / ranges(W) ? 0 : 1);
+  // Which of CTA c's two slots holds its piece of the unit starting at
+  // `start`: the first if the unit began before the CTA's range.
+  static __device__ __forceinline__ int slot(const Plan& p, int c, unsigned start) {
+    return 2 * c + (p.each || start < range_begin(c, p.total) ? 0 : 1);
   }
 };
 

@@ -184,6 +184,7 @@ def _rotary(mb):
     r = mb.Rotary.__new__(mb.Rotary)
     r.turns, r.rot, r.layout, r.amplitude = torch.zeros(hd // 2, dtype=torch.int64), hd, 0, 1.0
     r.c = mb.RotaryArgs(0, hd, r.turns.data_ptr(), 1.0)
+    r.ref = ctypes.byref(r.c)
     return r
 
 
