@@ -16,8 +16,8 @@
 // The maximum is moved (and O rescaled) only when a tile's exceeds it by more
 // than 2^8: any reference that keeps the exponents finite gives the same
 // quotient.  P is rounded to bf16 for the second product, which costs at most
-// half a bf16 step of each probability; the output, rounded to bf16 itself,
-// has no use for more.  Sums, maxima and O are fp32.
+// half a bf16 step of each probability, as much as rounding the output costs
+// it.  Sums, maxima and O are fp32.
 //
 // Tensor memory (512 columns): S_w at 128 w, its P (two keys per column) over
 // the first half of it, O_w at 256 + 128 w.  P V of a step is issued before
@@ -29,6 +29,7 @@
 // 4-11 are the two softmax warpgroups, a row per thread.  K and V tiles go
 // through one ring in the order in which they are used.  Every wait is bounded.
 #include <cudaTypedefs.h>
+#include <type_traits>
 
 #include "paged_work.cuh"
 #include "tcgen05.cuh"
@@ -111,6 +112,29 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// 2^x on the fp32 pipe, which has room while the exponential unit (16 a clock
+// and SM) does not: x = n + f with n the nearest integer (found by adding 1.5
+// 2^23) and |f| <= 1/2, 2^f by the cubic of least relative error on that
+// interval (7.5e-5, a fiftieth of half a bf16 step), n added to the exponent.
+// x <= 127; below -126 the result is 2^-126 (masked scores take the other way).
+__device__ __forceinline__ F2 exp2_poly(F2 x) {
+  float x0, x1;
+  unpair(x, x0, x1);
+  x = pair(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
+  const F2 magic = pair(12582912.f, 12582912.f), minus = pair(-1.f, -1.f);
+  const F2 t = add2(x, magic);
+  const F2 n = fma2(magic, minus, t), f = fma2(n, minus, x);
+  F2 q = pair(0.0551716685295105f, 0.0551716685295105f);
+  q = fma2(q, f, pair(0.2426111251115799f, 0.2426111251115799f));
+  q = fma2(q, f, pair(0.6932609677314758f, 0.6932609677314758f));
+  q = fma2(q, f, pair(0.9999280571937561f, 0.9999280571937561f));
+  float t0, t1, q0, q1;
+  unpair(t, t0, t1);
+  unpair(q, q0, q1);
+  return pair(__uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23)),
+              __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23)));
 }
 
 // What every role knows of a piece.
@@ -230,29 +254,17 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
     }
     tc::mma_commit(&bar->s_full[w]);
   };
-  // O_w += P_w V over the tile's first `chunks` groups of 32 keys.  Two-group
-  // units hold P in the first half of S's columns; alternating ones hold each
-  // chunk's P and its remainder in the chunk's own 32 columns.
-  auto values = [&](int w, int entry, bool first, bool pair, int chunks) {
+  // O_w += P_w V over the tile's first `chunks` groups of 32 keys.
+  auto values = [&](int w, int entry, bool first, int chunks) {
     if (!wait(&bar->p_full[w], np[w] & 1, bar, status)) return false;
     ++np[w];
     if (first && piece > 0 && !wait(&bar->o_free[w], (piece - 1) & 1, bar, status)) return false;
     if (!landed(entry)) return false;
     tc::fence_after_sync();
     const uint32_t vb = sbase + S::kOffRing + (entry % S::kStages) * S::kTile;
-    const uint32_t o = tmem + 256 + 128 * w, ps = tmem + 128 * w;
-    if (pair) {
-      for (int c = 0; c < chunks; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)          // P and remainder, 16 keys each
-          tc::mma_ts(o, ps + 32 * c + 16 * (k & 1) + 8 * (k >> 1),
-                     tc::smem_desc_sw128(vb + (2 * c + (k >> 1)) * 16 * 128, S::kHalf, 1024), idO,
-                     (!first || c > 0 || k > 0) ? 1u : 0u);
-    } else {
-#pragma unroll
-      for (int c = 0; c < kBK / 16; ++c)
-        tc::mma_ts(o, ps + c * 8, tc::smem_desc_sw128(vb + c * 16 * 128, S::kHalf, 1024), idO, (!first || c > 0) ? 1u : 0u);
-    }
+    for (int c = 0; c < 2 * chunks; ++c)
+      tc::mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + c * 8, tc::smem_desc_sw128(vb + c * 16 * 128, S::kHalf, 1024), idO,
+                 (!first || c > 0) ? 1u : 0u);
     tc::mma_commit(&bar->pv_done[w]);
     return true;
   };
@@ -275,13 +287,13 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
       }
       for (int i = 0; i < s.n; ++i) {
         const int v = e++;
-        if (!values(0, v, i == 0, false, 0)) return;
+        if (!values(0, v, i == 0, kBK / 32)) return;
         if (i + 1 < s.n) {
           if (!landed(e)) return;
           scores(0, 0, e);
           if (i + 2 == s.n) tc::mma_commit(&bar->q_empty[0]);
         }
-        if (!values(1, v, i == 0, false, 0)) return;
+        if (!values(1, v, i == 0, kBK / 32)) return;
         release(v);
         if (i + 1 < s.n) {
           scores(1, 1, e);
@@ -297,7 +309,7 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
       }
       if (s.n <= 2) tc::mma_commit(&bar->q_empty[0]);
       for (int i = 0; i < s.n; ++i) {
-        if (!values(i & 1, e, i < 2, true, tile_chunks(keys - (x.kb0 + i) * kBK))) return;
+        if (!values(i & 1, e, i < 2, tile_chunks(keys - (x.kb0 + i) * kBK))) return;
         release(e++);
         if (i + 2 < s.n) {
           if (!landed(e)) return;
@@ -490,31 +502,32 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         }
         const F2 sc = pair(p.scale_log2, p.scale_log2), rf = pair(ref, ref);
         F2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
+        // P, a quarter of it (in tiles without a mask) by the polynomial.
+        auto probabilities = [&](auto mixed) {
 #pragma unroll
-        for (int c = 0; c < kBK / 32; ++c) {
-          uint32_t hi[16];
-          float pv0[32];
+          for (int c = 0; c < kBK / 32; ++c) {
+            uint32_t pk[16];
 #pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            float a, d;
-            unpair(fma2(pair(sv[32 * c + k], sv[32 * c + k + 1]), sc, rf), a, d);
-            a = tc::ex2_ftz(a);
-            d = tc::ex2_ftz(d);
-            sum[(k >> 1) & 1] = add2(sum[(k >> 1) & 1], pair(a, d));
-            hi[k / 2] = pack2(a, d);
-            pv0[k] = a;
-            pv0[k + 1] = d;
+            for (int k = 0; k < 16; ++k) {
+              F2 y = fma2(pair(sv[32 * c + 2 * k], sv[32 * c + 2 * k + 1]), sc, rf);
+              float a, d;
+              if (decltype(mixed)::value && (k & 3) == 3) {
+                y = exp2_poly(y);
+                unpair(y, a, d);
+              } else {
+                unpair(y, a, d);
+                a = tc::ex2_ftz(a);
+                d = tc::ex2_ftz(d);
+                y = pair(a, d);
+              }
+              sum[k & 1] = add2(sum[k & 1], y);
+              pk[k] = pack2(a, d);
+            }
+            tc::tmem_st16(tS + 16 * c, pk);
           }
-          if (s.two) {
-            tc::tmem_st16(tS + 16 * c, hi);
-          } else {
-            uint32_t lo[16];                 // the remainder of P
-#pragma unroll
-            for (int k = 0; k < 16; ++k) lo[k] = pack2(pv0[2 * k] - bf16lo(hi[k]), pv0[2 * k + 1] - bf16hi(hi[k]));
-            tc::tmem_st16(tS + 32 * c, hi);
-            tc::tmem_st16(tS + 32 * c + 16, lo);
-          }
-        }
+        };
+        if (j0 + kBK > clear) probabilities(std::false_type{});
+        else probabilities(std::true_type{});
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
         l = l * factor + (s0 + s1);
