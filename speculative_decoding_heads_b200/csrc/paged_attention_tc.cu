@@ -59,7 +59,7 @@ struct Shape {
 struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2];
-  uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2];
   uint64_t stat_full, stat_free, group[2];   // statistics handed over; the threads of one warpgroup
   uint32_t tmem_base;
   int abort, last[2];
@@ -81,11 +81,14 @@ struct Params {
   uint16_t* out;
 };
 
+// A whole warp waits and agrees on the outcome (a wait that runs out in one
+// lane ends the role for all of them).
 __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, int* status) {
-  if (b->abort) return false;
-  if (mbar_wait(bar, parity)) return true;
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const bool ok = *reinterpret_cast<volatile int*>(&b->abort) == 0 && mbar_wait(bar, parity);
+  if (__all_sync(0xffffffffu, ok)) return true;
   set_device_status(status, MEDUSA_ERR_TIMEOUT, kDetailPagedWait);
-  b->abort = 1;
+  *reinterpret_cast<volatile int*>(&b->abort) = 1;
   return false;
 }
 
@@ -233,7 +236,16 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
     if (nq[w] > 0) mbar_wait(&bar->q_full[w], (nq[w] - 1) & 1);
 }
 
-// ---- products (warp 1, one thread) -----------------------------------------
+// ---- products (warp 1) -------------------------------------------------------
+// The whole warp waits, so that addresses stay in uniform registers, and the
+// elected lane (always the same one) issues: a thread that computed every
+// descriptor on its own path took as long to issue a product as to run it.
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+  return ok != 0;
+}
 
 template <int HD>
 __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bars* bar, Piece x, unsigned left) {
@@ -242,80 +254,105 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
   constexpr uint32_t idO = tc::idesc_bf16_f32(kGroup, HD, 1);
   const Plan& pl = bar->plan;
   int* status = p.w.status;
-  int e = 0, nq[2] = {0, 0}, np[2] = {0, 0}, piece = 0;
-  auto landed = [&](int entry) { return wait(&bar->full[entry % S::kStages], (entry / S::kStages) & 1, bar, status); };
-  auto scores = [&](int w, int q, int entry) {            // S_w = Q_q K^T
-    tc::fence_after_sync();
-    const uint32_t kb = sbase + S::kOffRing + (entry % S::kStages) * S::kTile, qb = sbase + q * S::kTile;
-#pragma unroll
-    for (int c = 0; c < HD / 16; ++c) {
-      const uint32_t off = (c >> 2) * S::kHalf + (c & 3) * 32;
-      tc::mma_ss(tmem + 128 * w, tc::smem_desc_sw128(qb + off, 16, 1024), tc::smem_desc_sw128(kb + off, 16, 1024), idS, c > 0);
+  int st = 0, ph = 0;                        // the next ring entry's stage and parity
+  int nq[2] = {0, 0}, np[2] = {0, 0}, piece = 0;
+  const uint32_t ring = sbase + S::kOffRing;
+  // Descriptors of a tile's first 16 columns (Q, K) or keys (V); the others add to the address field.
+  const uint64_t q0 = tc::smem_desc_sw128(sbase, 16, 1024), k0 = tc::smem_desc_sw128(ring, 16, 1024),
+                 v0 = tc::smem_desc_sw128(ring, S::kHalf, 1024);
+  auto next = [&] {
+    if (++st == S::kStages) {
+      st = 0;
+      ph ^= 1;
     }
-    tc::mma_commit(&bar->s_full[w]);
   };
-  // O_w += P_w V over the tile's first `chunks` groups of 32 keys.
-  auto values = [&](int w, int entry, bool first, int chunks) {
+  auto landed = [&] { return wait(&bar->full[st], ph, bar, status); };
+  auto scores = [&](int w, int q, bool release, bool last) {          // S_w = Q_q K^T
+    const uint64_t qd = q0 + q * (S::kTile >> 4), kd = k0 + static_cast<uint64_t>(st) * (S::kTile >> 4);
+    tc::fence_after_sync();
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < HD / 16; ++c) {
+        const uint32_t off = ((c >> 2) * S::kHalf + (c & 3) * 32) >> 4;
+        tc::mma_ss(tmem + 128 * w, qd + off, kd + off, idS, c > 0);
+      }
+      tc::mma_commit(&bar->s_full[w]);
+      if (release) tc::mma_commit(&bar->empty[st]);
+      if (last) tc::mma_commit(&bar->q_empty[q]);
+    }
+    __syncwarp();
+  };
+  // O_w += P_w V over the tile's first `chunks` groups of 32 keys; the second half of P follows on its own.
+  auto values = [&](int w, bool first, int chunks, bool release) {
+    const uint64_t vd = v0 + static_cast<uint64_t>(st) * (S::kTile >> 4);
+    const uint32_t o = tmem + 256 + 128 * w, ps = tmem + 128 * w;
+    if (!landed()) return false;
+    if (first && piece > 0 && !wait(&bar->o_free[w], (piece - 1) & 1, bar, status)) return false;
+    if (!wait(&bar->p_half[w], np[w] & 1, bar, status)) return false;
+    tc::fence_after_sync();
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < 2 * chunks) tc::mma_ts(o, ps + c * 8, vd + c * (16 * 128 >> 4), idO, (!first || c > 0) ? 1u : 0u);
+    }
+    __syncwarp();
     if (!wait(&bar->p_full[w], np[w] & 1, bar, status)) return false;
     ++np[w];
-    if (first && piece > 0 && !wait(&bar->o_free[w], (piece - 1) & 1, bar, status)) return false;
-    if (!landed(entry)) return false;
     tc::fence_after_sync();
-    const uint32_t vb = sbase + S::kOffRing + (entry % S::kStages) * S::kTile;
-    for (int c = 0; c < 2 * chunks; ++c)
-      tc::mma_ts(tmem + 256 + 128 * w, tmem + 128 * w + c * 8, tc::smem_desc_sw128(vb + c * 16 * 128, S::kHalf, 1024), idO,
-                 (!first || c > 0) ? 1u : 0u);
-    tc::mma_commit(&bar->pv_done[w]);
+    if (elect_one()) {
+#pragma unroll
+      for (int c = 4; c < 8; ++c)
+        if (c < 2 * chunks) tc::mma_ts(o, ps + c * 8, vd + c * (16 * 128 >> 4), idO, 1u);
+      tc::mma_commit(&bar->pv_done[w]);
+      if (release) tc::mma_commit(&bar->empty[st]);
+    }
+    __syncwarp();
     return true;
   };
-  auto release = [&](int entry) { tc::mma_commit(&bar->empty[entry % S::kStages]); };
   for (;;) {
     const Seg s = segment(p, pl, x);
     const int keys = C::keys(p.w, pl, x.b, x.tile);
     if (!wait(&bar->q_full[0], nq[0] & 1, bar, status)) return;
     ++nq[0];
     if (s.two) {
-      if (!landed(e)) return;
-      scores(0, 0, e);
+      if (!landed()) return;
+      scores(0, 0, false, s.n == 1);
       if (!wait(&bar->q_full[1], nq[1] & 1, bar, status)) return;
       ++nq[1];
-      scores(1, 1, e);
-      release(e++);
-      if (s.n == 1) {
-        tc::mma_commit(&bar->q_empty[0]);
-        tc::mma_commit(&bar->q_empty[1]);
-      }
+      scores(1, 1, true, s.n == 1);
+      next();
       for (int i = 0; i < s.n; ++i) {
-        const int v = e++;
-        if (!values(0, v, i == 0, kBK / 32)) return;
-        if (i + 1 < s.n) {
-          if (!landed(e)) return;
-          scores(0, 0, e);
-          if (i + 2 == s.n) tc::mma_commit(&bar->q_empty[0]);
+        // V_i serves both groups, K_{i+1} behind it in the ring too.
+        const bool more = i + 1 < s.n;
+        const int vst = st, vph = ph;
+        if (!values(0, i == 0, kBK / 32, false)) return;
+        if (more) {
+          next();
+          if (!landed()) return;
+          scores(0, 0, false, i + 2 == s.n);
+          st = vst;
+          ph = vph;
         }
-        if (!values(1, v, i == 0, kBK / 32)) return;
-        release(v);
-        if (i + 1 < s.n) {
-          scores(1, 1, e);
-          if (i + 2 == s.n) tc::mma_commit(&bar->q_empty[1]);
-          release(e++);
+        if (!values(1, i == 0, kBK / 32, true)) return;
+        next();
+        if (more) {
+          scores(1, 1, true, i + 2 == s.n);
+          next();
         }
       }
     } else {
       for (int i = 0; i < 2 && i < s.n; ++i) {
-        if (!landed(e)) return;
-        scores(i, 0, e);
-        release(e++);
+        if (!landed()) return;
+        scores(i, 0, true, i + 1 == s.n);
+        next();
       }
-      if (s.n <= 2) tc::mma_commit(&bar->q_empty[0]);
       for (int i = 0; i < s.n; ++i) {
-        if (!values(i & 1, e, i < 2, tile_chunks(keys - (x.kb0 + i) * kBK))) return;
-        release(e++);
+        if (!values(i & 1, i < 2, tile_chunks(keys - (x.kb0 + i) * kBK), true)) return;
+        next();
         if (i + 2 < s.n) {
-          if (!landed(e)) return;
-          scores(i & 1, 0, e);
-          release(e++);
-          if (i + 3 == s.n) tc::mma_commit(&bar->q_empty[0]);
+          if (!landed()) return;
+          scores(i & 1, 0, true, i + 3 == s.n);
+          next();
         }
       }
     }
@@ -453,10 +490,16 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
     const int limit = L + min(tok, n - 1) + 1;
     const int clear = tree ? L : L + grp_row / p.w.g + 1;
     float m = -INFINITY, l = 0.f;
+    auto hand_over = [&](uint64_t* to) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(to);
+    };
     for (int i = s.two ? 0 : w; i < s.n; i += s.two ? 1 : 2, ++steps) {
       if (!wait(&bar->s_full[w], steps & 1, bar, status)) return;
       tc::fence_after_sync();
       const int j0 = (x.kb0 + i) * kBK;
+      const bool zero = (w == 0 || !s.two) && x.kb0 + i == x.blocks - 1 && (keys & (p.box - 1)) != 0;
       if (active) {
         float sv[kBK];
 #pragma unroll
@@ -524,6 +567,10 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
               pk[k] = pack2(a, d);
             }
             tc::tmem_st16(tS + 16 * c, pk);
+            if (c == 1 && !zero) {           // the first half of P V can start
+              tc::tmem_wait_st();
+              hand_over(&bar->p_half[w]);
+            }
           }
         };
         if (j0 + kBK > clear) probabilities(std::false_type{});
@@ -533,7 +580,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         l = l * factor + (s0 + s1);
         tc::tmem_wait_st();
       }
-      if ((w == 0 || !s.two) && x.kb0 + i == x.blocks - 1 && (keys & (p.box - 1)) != 0) {
+      if (zero) {
         // Rows of the last page past the sequence may hold anything: zero
         // their values, so that 0 * (stale value) stays 0.
         const int v = entries + 2 * s.n - 1;            // a piece's last ring entry
@@ -545,9 +592,8 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           for (int hf = 0; hf < S::kHalves; ++hf) *reinterpret_cast<uint4*>(d + hf * S::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
         tc::fence_proxy_async_smem();
       }
-      tc::fence_before_sync();
-      __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar->p_full[w]);
+      if (zero || !active) hand_over(&bar->p_half[w]);
+      hand_over(&bar->p_full[w]);
     }
 
     // Output, a row per thread.  Where the tiles alternated, the second
@@ -687,6 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bar->q_full[w], 1);
         mbar_init(&bar->q_empty[w], 1);
         mbar_init(&bar->s_full[w], 1);
+        mbar_init(&bar->p_half[w], 4);
         mbar_init(&bar->p_full[w], 4);
         mbar_init(&bar->pv_done[w], 1);
         mbar_init(&bar->o_free[w], 4);
@@ -721,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc::fence_before_sync();
     asm volatile("barrier.cta.sync 1, 384;" ::: "memory");
     tc::fence_after_sync();
-    if (tid == 32 && bar->plan.begin < bar->plan.end) {
+    if (warp == 1 && bar->plan.begin < bar->plan.end) {
       unsigned left;
       const Piece x = C::first_piece(p.w, bar->plan, left);
       run_products<HD>(p, smem_u32(smem), bar->tmem_base, bar, x, left);
