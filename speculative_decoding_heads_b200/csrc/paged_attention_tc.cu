@@ -388,69 +388,80 @@ __device__ __forceinline__ float4* slot_out(float* slot, int row, int col4) {
 }
 
 // Joins the pieces that CTAs lo..hi left of a unit's row group (128 threads):
-// out = sum_y 2^(m_y - lse) O_y, lse = m + log2 sum_y 2^(m_y - m) l_y.  First a
-// thread per row finds lse; then a thread owns row thread % 8 of four blocks
-// of eight rows and every 16th group of columns, all its loads of four pieces
-// in flight together (the pieces come from L2).
-__device__ __forceinline__ float join_lse(const Work& w, const Plan& pl, unsigned start, int lo, int hi, int slot_row, int floats) {
-  float m = -INFINITY, l = 0.f;
-#pragma unroll 8
-  for (int y = lo; y <= hi; ++y) m = fmaxf(m, __ldcg(w.slots + static_cast<size_t>(C::slot(pl, y, start)) * floats + slot_row));
-  const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll 8
-  for (int y = lo; y <= hi; ++y) {
-    const float* slot = w.slots + static_cast<size_t>(C::slot(pl, y, start)) * floats + slot_row;
-    l = fmaf(tc::ex2_ftz(__ldcg(slot) - ref), __ldcg(slot + 2 * kGroup), l);
-  }
-  return ref + __log2f(l);
-}
-
-template <int HD, typename Put>
-__device__ __forceinline__ void join(const Work& w, const Plan& pl, unsigned start, int lo, int hi, int row0, int thread,
-                                     int rows, const float* lse, Put put) {
+// out = sum_y 2^(m_y - m) O_y / sum_y 2^(m_y - m) l_y.  A thread owns row
+// thread % 8 of kRB blocks of eight rows and every 16th group of columns; the
+// loads of kPB pieces (from L2) are in flight together.
+template <int HD, int kRB, int kPB, typename Put>
+__device__ __forceinline__ void join_rows(const Work& w, const Plan& pl, unsigned start, int lo, int hi, int row0, int thread,
+                                          int rows, Put put) {
   constexpr int kCols = HD / 64;             // column groups per thread and row
   const int r8 = thread & 7, c4 = thread >> 3;
-  for (int rb = 0; rb < rows; rb += 32) {
-    const int blocks = min(4, (rows - rb + 7) >> 3);
-    float4 o[4][kCols];
-    float ref[4];
+  for (int rb = 0; rb < rows; rb += 8 * kRB) {
+    float m[kRB], l[kRB];
+    float4 o[kRB][kCols];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      ref[i] = i < blocks ? lse[rb + 8 * i + r8] : 0.f;
+    for (int i = 0; i < kRB; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
 #pragma unroll
       for (int k = 0; k < kCols; ++k) o[i][k] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-#pragma unroll 4
-    for (int y = lo; y <= hi; ++y) {
-      float* slot = w.slots + static_cast<size_t>(C::slot(pl, y, start)) * slot_floats(2 * kGroup, HD);
+#pragma unroll 1
+    for (int y0 = lo; y0 <= hi; y0 += kPB) {
+      float ms[kRB][kPB], ls[kRB][kPB];
+      float4 os[kRB][kPB][kCols];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = row0 + rb + 8 * i + r8;
-        float f = 0.f;
-        float4 v4[kCols];
-        if (i < blocks) {
-          f = tc::ex2_ftz(__ldcg(slot + row) - ref[i]);
+      for (int y = 0; y < kPB; ++y) {
+        float* slot = w.slots + static_cast<size_t>(C::slot(pl, y0 + y <= hi ? y0 + y : hi, start)) * slot_floats(2 * kGroup, HD);
 #pragma unroll
-          for (int k = 0; k < kCols; ++k) v4[k] = __ldcg(slot_out<HD>(slot, row, c4 + 16 * k));
-        } else {
+        for (int i = 0; i < kRB; ++i) {
+          const int r = rb + 8 * i + r8, row = row0 + r;
+          ms[i][y] = -INFINITY;
+          ls[i][y] = 0.f;
 #pragma unroll
-          for (int k = 0; k < kCols; ++k) v4[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int k = 0; k < kCols; ++k) os[i][y][k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (y0 + y <= hi && r < rows) {
+            ms[i][y] = __ldcg(slot + row);
+            ls[i][y] = __ldcg(slot + 2 * kGroup + row);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) os[i][y][k] = __ldcg(slot_out<HD>(slot, row, c4 + 16 * k));
+          }
         }
+      }
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) {
-          const float4 v = v4[k];
-          o[i][k].x = fmaf(f, v.x, o[i][k].x);
-          o[i][k].y = fmaf(f, v.y, o[i][k].y);
-          o[i][k].z = fmaf(f, v.z, o[i][k].z);
-          o[i][k].w = fmaf(f, v.w, o[i][k].w);
+      for (int i = 0; i < kRB; ++i) {
+        float mn = m[i];
+#pragma unroll
+        for (int y = 0; y < kPB; ++y) mn = fmaxf(mn, ms[i][y]);
+        const float ref = mn == -INFINITY ? 0.f : mn, keep = tc::ex2_ftz(m[i] - ref);
+        m[i] = mn;
+        l[i] *= keep;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+          o[i][k] = make_float4(o[i][k].x * keep, o[i][k].y * keep, o[i][k].z * keep, o[i][k].w * keep);
+#pragma unroll
+        for (int y = 0; y < kPB; ++y) {
+          const float f = tc::ex2_ftz(ms[i][y] - ref);
+          l[i] = fmaf(f, ls[i][y], l[i]);
+#pragma unroll
+          for (int k = 0; k < kCols; ++k) {
+            o[i][k].x = fmaf(f, os[i][y][k].x, o[i][k].x);
+            o[i][k].y = fmaf(f, os[i][y][k].y, o[i][k].y);
+            o[i][k].z = fmaf(f, os[i][y][k].z, o[i][k].z);
+            o[i][k].w = fmaf(f, os[i][y][k].w, o[i][k].w);
+          }
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < blocks)
+    for (int i = 0; i < kRB; ++i) {
+      const int r = rb + 8 * i + r8;
+      const float inv = 1.f / l[i];
+      if (r < rows)
 #pragma unroll
-        for (int k = 0; k < kCols; ++k) put(rb + 8 * i + r8, 4 * (c4 + 16 * k), o[i][k].x, o[i][k].y, o[i][k].z, o[i][k].w);
+        for (int k = 0; k < kCols; ++k)
+          put(r, 4 * (c4 + 16 * k), make_uint2(pack2(o[i][k].x * inv, o[i][k].y * inv), pack2(o[i][k].z * inv, o[i][k].w * inv)));
+    }
   }
 }
 
@@ -470,7 +481,6 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
   int entries = 0;                           // ring entries before this piece
   int syncs = 0;                             // uses of this warpgroup's barrier
   int singles = 0;                           // alternating pieces before this one
-  int piece = 0;                             // pieces before this one
   for (;;) {
     const Seg s = segment(p, pl, x);
     const int b = x.b, L = pl.L[b], n = pl.n[b];
@@ -604,14 +614,15 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
     float f0 = 1.f, f1 = 0.f;
     if (!s.two) {
       if (w == 1) {
-        // the first warpgroup is done with the piece before
-        if (piece > 0 && !wait(&bar->stat_free, (piece - 1) & 1, bar, status)) return;
+        // the first warpgroup has read the last hand-over
+        if (singles > 0 && !wait(&bar->stat_free, (singles - 1) & 1, bar, status)) return;
         bar->m1[row] = m;
         bar->l1[row] = l;
         tc::mbar_arrive(&bar->stat_full);
       } else {
         if (!wait(&bar->stat_full, singles & 1, bar, status)) return;
         const float m1 = bar->m1[row], l1 = bar->l1[row], mm = fmaxf(m, m1);
+        tc::mbar_arrive(&bar->stat_free);
         f0 = m == -INFINITY ? 0.f : tc::ex2_ftz(m - mm);
         f1 = m1 == -INFINITY ? 0.f : tc::ex2_ftz(m1 - mm);
         m = mm;
@@ -630,11 +641,9 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
       uint16_t* dst = p.out + (static_cast<size_t>(pl.first[b] + tok) * p.w.H + x.h * p.w.g + (grp_row + row - tok * p.w.g)) * HD;
       const float inv = 1.f / l;
       // Columns c .. c + 3 of row r of the group.
-      auto put = [&](int r, int c, float a, float d, float e, float f) {
-        if (r >= rows) return;
+      auto put = [&](int r, int c, uint2 v) {
         const int t = (grp_row + r) / p.w.g;
-        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(pl.first[b] + t) * p.w.H + x.h * p.w.g + (grp_row + r - t * p.w.g)) * HD + c) =
-            make_uint2(pack2(a, d), pack2(e, f));
+        *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(pl.first[b] + t) * p.w.H + x.h * p.w.g + (grp_row + r - t * p.w.g)) * HD + c) = v;
       };
       if (active) {
 #pragma unroll 1
@@ -688,21 +697,15 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
         if (bar->last[w]) {
           __threadfence();
-          // The hand-over arrays hold the rows' lse: the first's maxima are its
-          // own until it frees them, the second waits for that.
-          float* lse = w == 0 ? bar->m1 : bar->l1;
-          if (w == 1 && piece > 0 && !wait(&bar->stat_free, (piece - 1) & 1, bar, status)) return;
-          lse[row] = row < rows ? join_lse(p.w, pl, x.start, lo, hi, slot_row, static_cast<int>(slot_floats(2 * kGroup, HD))) : 0.f;
-          tc::mbar_arrive(&bar->group[w]);
-          if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
-          join<HD>(p.w, pl, x.start, lo, hi, s.two ? w * kGroup : 0, row, rows, lse, put);
+          const int row0 = s.two ? w * kGroup : 0;
+          // Few rows or many pieces: more pieces at a time; else more rows.
+          if (rows <= 16 || hi - lo >= 6) join_rows<HD, 2, 4>(p.w, pl, x.start, lo, hi, row0, row, rows, put);
+          else join_rows<HD, 4, 2>(p.w, pl, x.start, lo, hi, row0, row, rows, put);
         }
       }
     }
-    if (w == 0) tc::mbar_arrive(&bar->stat_free);
     pv[0] += n0;
     pv[1] += n1;
-    ++piece;
     if (left == 0) return;
     C::next_piece(p.w, pl, x, left);
   }

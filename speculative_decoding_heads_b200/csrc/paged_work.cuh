@@ -43,7 +43,6 @@ struct Work {
 
 struct Plan {
   int L[MEDUSA_MAX_B], n[MEDUSA_MAX_B], first[MEDUSA_MAX_B];
-  int tile0[MEDUSA_MAX_B + 1];         // tiles of the sequences before
   unsigned total;                      // W: key blocks of all units
   unsigned each;                       // cut at unit boundaries: blocks per CTA; 0: equal ranges
   unsigned begin, end;                 // this CTA's range
@@ -58,24 +57,23 @@ struct Piece {
   unsigned start;              // offset of the unit in the whole list
 };
 
-// sum_{i=0}^{n-1} floor((a i + b) / m)
-__device__ __forceinline__ unsigned long long floor_sum(unsigned long long n, unsigned long long m, unsigned long long a,
-                                                        unsigned long long b) {
+// sum_{i=0}^{n-1} floor((a i + b) / m); a n + b below 2^32.
+__device__ __forceinline__ unsigned long long floor_sum(unsigned n, unsigned m, unsigned a, unsigned b) {
   unsigned long long s = 0;
   while (n > 0) {
     if (a >= m) {
-      s += n * (n - 1) / 2 * (a / m);
+      s += static_cast<unsigned long long>(n) * (n - 1) / 2 * (a / m);
       a %= m;
     }
     if (b >= m) {
-      s += n * (b / m);
+      s += static_cast<unsigned long long>(n) * (b / m);
       b %= m;
     }
-    const unsigned long long y = a * n + b;   // the line's height: count its lattice points from the other axis
+    const unsigned y = a * n + b;             // the line's height: count its lattice points from the other axis
     if (y < m) break;
     n = y / m;
     b = y % m;
-    const unsigned long long t = m;
+    const unsigned t = m;
     m = a;
     a = t;
   }
@@ -99,12 +97,14 @@ struct Cut {
     const unsigned long long all = (static_cast<unsigned>(L) + n + BK - 1) / BK;
     if (t == 0) return 0ull;
     if (w.t.T > 0) return all * t;
-    const unsigned long long m = static_cast<unsigned long long>(w.g) * BK;
+    // With L = BK q + r the quotients are q + ceil((g r + i R) / (g BK)): 32 bits suffice (t R < 2^31).
+    const unsigned m = w.g * BK, q = static_cast<unsigned>(L) / BK, r = static_cast<unsigned>(L) % BK;
     const int k = t < tiles ? t : tiles - 1;     // the last tile ends with the chunk
     const unsigned long long s =
-        k == 0 ? 0ull : floor_sum(k, m, w.R, static_cast<unsigned long long>(w.g) * L + w.R + m - 1);
+        k == 0 ? 0ull : static_cast<unsigned long long>(k) * q + floor_sum(k, m, w.R, w.g * r + w.R + m - 1);
     return t < tiles ? s : s + all;
   }
+  static __device__ __forceinline__ int tiles_of(const Work& w, int n) { return (n * w.g + w.R - 1) / w.R; }
 
   // One whole warp; the other threads see the plan after the next __syncthreads.
   static __device__ void plan(const Work& w, Plan& p) {
@@ -113,22 +113,24 @@ struct Cut {
     int L[2], n[2], tiles[2];
     unsigned long long work[2];
     const long long cap = static_cast<long long>(w.kv.max_pages) << w.kv.page_shift;
-    bool bad = false;
+    bool bad = false, descends = false;
+    int first[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int b = 2 * lane + i;
-      int first = 0;
+      first[i] = 0;
       L[i] = n[i] = 0;
       if (b < B) {
         L[i] = w.kv.lens[b];
         if (w.starts) {
-          first = w.starts[b];
-          n[i] = w.starts[b + 1] - first;
+          first[i] = w.starts[b];
+          n[i] = w.starts[b + 1] - first[i];
+          descends |= n[i] < 0;
         } else {
           n[i] = w.N / B;
-          first = n[i] * b;
+          first[i] = n[i] * b;
         }
-        const bool ok = n[i] == 0 || (n[i] > 0 && first >= 0 && first <= w.N - n[i] && L[i] >= 0 &&
+        const bool ok = n[i] == 0 || (n[i] > 0 && first[i] >= 0 && first[i] <= w.N - n[i] && L[i] >= 0 &&
                                       static_cast<long long>(L[i]) + n[i] <= cap &&
                                       static_cast<long long>(L[i]) + n[i] < 0x7fffff00ll);
         if (!ok) {
@@ -136,10 +138,16 @@ struct Cut {
           bad = true;
         }
       }
+    }
+    const bool none = __any_sync(0xffffffffu, descends);   // overlapping chunks: nothing is computed
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int b = 2 * lane + i;
+      if (none) n[i] = 0;
       p.L[b] = L[i];
       p.n[b] = n[i];
-      p.first[b] = first;
-      tiles[i] = (n[i] * w.g + w.R - 1) / w.R;
+      p.first[b] = first[i];
+      tiles[i] = tiles_of(w, n[i]);
       work[i] = n[i] > 0 ? before_tile(w, L[i], n[i], tiles[i], tiles[i]) * hk : 0ull;
     }
     // Tiles (below 2^23) and blocks, summed over the lanes before in one word.
@@ -150,10 +158,6 @@ struct Cut {
       if (lane >= o) both += v;
     }
     const unsigned long long ws = both >> 23;
-    const int ts = static_cast<int>(both & 0x7fffffu);
-    p.tile0[2 * lane + 1] = ts - tiles[1];
-    p.tile0[2 * lane + 2] = ts;
-    if (lane == 0) p.tile0[0] = 0;
     both = __shfl_sync(0xffffffffu, both, 31);
     unsigned long long W = both >> 23;
     if (W > 0x7fffffffull) {     // 2^31 blocks of keys in one call: refused like any other impossible chunk
@@ -213,30 +217,31 @@ struct Cut {
     if (begin >= end) return;
     // The lane whose sequences hold offset begin, and where in them it lies.
     unsigned long long off = ws - work[0] - work[1];      // blocks before this lane's sequences
-    const bool mine = begin >= off && begin < ws;
-    if (mine) {
-      const int i = begin >= off + work[0] ? 1 : 0;
-      if (i) off += work[0];
-      const unsigned rem = begin - static_cast<unsigned>(off), per_head = static_cast<unsigned>(i ? work[1] : work[0]) / hk;
-      const int h = rem / per_head;
-      const unsigned at = rem - h * per_head;
-      const int Li = i ? L[1] : L[0], ni = i ? n[1] : n[0], nt = i ? tiles[1] : tiles[0];
-      int lo = 0, hi = nt;                                // largest tile with before_tile(tile) <= at
-      unsigned long long at_lo = 0ull;
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        const unsigned long long s = before_tile(w, Li, ni, nt, mid);
-        if (s <= at) {
-          lo = mid;
-          at_lo = s;
-        } else {
-          hi = mid;
-        }
-      }
+    const int src = __ffs(__ballot_sync(0xffffffffu, begin >= off && begin < ws)) - 1;
+    const int i = begin >= off + work[0] ? 1 : 0;
+    if (i) off += work[0];
+    const unsigned rem = begin - static_cast<unsigned>(off), per_head = static_cast<unsigned>(i ? work[1] : work[0]) / hk;
+    const unsigned head = per_head > 0 ? rem / per_head : 0u;
+    const unsigned at = __shfl_sync(0xffffffffu, rem - head * per_head, src);
+    const int Li = __shfl_sync(0xffffffffu, i ? L[1] : L[0], src), ni = __shfl_sync(0xffffffffu, i ? n[1] : n[0], src);
+    const int nt = __shfl_sync(0xffffffffu, i ? tiles[1] : tiles[0], src);
+    // The largest tile with before_tile(tile) <= at: all lanes probe, 32 tiles apart by powers of 32.
+    int lo = 0;
+    unsigned at_lo = 0u;
+    int step = 1;
+    while (step * 32 < nt) step *= 32;
+    for (; nt > 1 && step > 0; step /= 32) {
+      const long long t = lo + static_cast<long long>(lane) * step;
+      const unsigned long long s = t < nt ? before_tile(w, Li, ni, nt, static_cast<int>(t)) : ~0ull;
+      const int k = 31 - __clz(__ballot_sync(0xffffffffu, s <= at));   // lane 0's always is
+      lo += k * step;
+      at_lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(s), k);
+    }
+    if (lane == src) {
       p.b = 2 * lane + i;
-      p.h = h;
+      p.h = static_cast<int>(head);
       p.tile = lo;
-      p.block = static_cast<int>(at - static_cast<unsigned>(at_lo));
+      p.block = static_cast<int>(at - at_lo);
     }
   }
 
@@ -273,7 +278,7 @@ struct Cut {
   static __device__ __forceinline__ void next_piece(const Work& w, const Plan& p, Piece& x, unsigned& left) {
     x.start += x.blocks;
     x.kb0 = 0;
-    if (++x.tile == p.tile0[x.b + 1] - p.tile0[x.b]) {
+    if (++x.tile == tiles_of(w, p.n[x.b])) {
       x.tile = 0;
       if (++x.h == w.kv.Hkv) {
         x.h = 0;
@@ -291,8 +296,10 @@ struct Cut {
   }
   static __device__ __forceinline__ bool whole(const Piece& x) { return x.kb0 == 0 && x.kb1 == x.blocks; }
 
+  // Chunks do not overlap, so floor(first g / R) + b starts a sequence's tiles clear of the one before.
   static __device__ __forceinline__ unsigned* counter(const Work& w, const Plan& p, const Piece& x) {
-    return w.counters + (static_cast<size_t>(p.tile0[x.b] + x.tile) * w.kv.Hkv + x.h) * kCounters;
+    const int tile0 = p.first[x.b] * w.g / w.R + x.b;
+    return w.counters + (static_cast<size_t>(tile0 + x.tile) * w.kv.Hkv + x.h) * kCounters;
   }
   // Which of CTA c's two slots holds its piece of the unit starting at
   // `start`: the first if the unit began before the CTA's range.
@@ -304,7 +311,7 @@ struct Cut {
 // Bytes of the counters (for the largest possible number of units) and floats
 // of a slot (R rows of hd outputs, a maximum and a sum).
 inline size_t counter_bytes(int N, int H, int Hkv, int B, int R) {
-  const long long tiles = (static_cast<long long>(N) * (H / Hkv) + R - 1) / R + B;
+  const long long tiles = static_cast<long long>(N) * (H / Hkv) / R + B + 1;
   return align_up(static_cast<size_t>(tiles) * Hkv * kCounters * sizeof(unsigned), 256);
 }
 constexpr size_t slot_floats(int R, int hd) { return static_cast<size_t>(R) * (hd + 2); }

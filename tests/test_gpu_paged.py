@@ -221,6 +221,7 @@ ATTN = [
     ("bf16", 128, 128, 5, 1, [0, 300], [301, 64]),
     ("bf16", 128, 64, 3, 1, [511], [129]),
     ("bf16", 128, 64, 32, 2, [63], [9]),
+    ("bf16", 128, 64, 8, 2, [300], [2048]),      # many tiles to a CTA, whole ones and pieces, one key tile and more
     ("bf16", 64, 16, 4, 2, [100, 5], [3, 140]),
     ("bf16", 64, 64, 9, 3, [1500, 3], [1, 1]),
     ("bf16", 96, 16, 2, 2, [70], [20]),
