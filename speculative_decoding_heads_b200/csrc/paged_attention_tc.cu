@@ -29,7 +29,6 @@
 // 4-11 are the two softmax warpgroups, a row per thread.  K and V tiles go
 // through one ring in the order in which they are used.  Every wait is bounded.
 #include <cudaTypedefs.h>
-#include <type_traits>
 
 #include "paged_work.cuh"
 #include "tcgen05.cuh"
@@ -115,29 +114,6 @@ __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
-}
-
-// 2^x on the fp32 pipe, which has room while the exponential unit (16 a clock
-// and SM) does not: x = n + f with n the nearest integer (found by adding 1.5
-// 2^23) and |f| <= 1/2, 2^f by the cubic of least relative error on that
-// interval (7.5e-5, a fiftieth of half a bf16 step), n added to the exponent.
-// x <= 127; below -126 the result is 2^-126 (masked scores take the other way).
-__device__ __forceinline__ F2 exp2_poly(F2 x) {
-  float x0, x1;
-  unpair(x, x0, x1);
-  x = pair(fmaxf(x0, -126.f), fmaxf(x1, -126.f));
-  const F2 magic = pair(12582912.f, 12582912.f), minus = pair(-1.f, -1.f);
-  const F2 t = add2(x, magic);
-  const F2 n = fma2(magic, minus, t), f = fma2(n, minus, x);
-  F2 q = pair(0.0551716685295105f, 0.0551716685295105f);
-  q = fma2(q, f, pair(0.2426111251115799f, 0.2426111251115799f));
-  q = fma2(q, f, pair(0.6932609677314758f, 0.6932609677314758f));
-  q = fma2(q, f, pair(0.9999280571937561f, 0.9999280571937561f));
-  float t0, t1, q0, q1;
-  unpair(t, t0, t1);
-  unpair(q, q0, q1);
-  return pair(__uint_as_float(__float_as_uint(q0) + (__float_as_uint(t0) << 23)),
-              __uint_as_float(__float_as_uint(q1) + (__float_as_uint(t1) << 23)));
 }
 
 // What every role knows of a piece.
@@ -555,36 +531,24 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         }
         const F2 sc = pair(p.scale_log2, p.scale_log2), rf = pair(ref, ref);
         F2 sum[2] = {pair(0.f, 0.f), pair(0.f, 0.f)};
-        // P, a quarter of it (in tiles without a mask) by the polynomial.
-        auto probabilities = [&](auto mixed) {
 #pragma unroll
-          for (int c = 0; c < kBK / 32; ++c) {
-            uint32_t pk[16];
+        for (int c = 0; c < kBK / 32; ++c) {
+          uint32_t pk[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              F2 y = fma2(pair(sv[32 * c + 2 * k], sv[32 * c + 2 * k + 1]), sc, rf);
-              float a, d;
-              if (decltype(mixed)::value && (k & 3) == 3) {
-                y = exp2_poly(y);
-                unpair(y, a, d);
-              } else {
-                unpair(y, a, d);
-                a = tc::ex2_ftz(a);
-                d = tc::ex2_ftz(d);
-                y = pair(a, d);
-              }
-              sum[k & 1] = add2(sum[k & 1], y);
-              pk[k] = pack2(a, d);
-            }
-            tc::tmem_st16(tS + 16 * c, pk);
-            if (c == 1 && !zero) {           // the first half of P V can start
-              tc::tmem_wait_st();
-              hand_over(&bar->p_half[w]);
-            }
+          for (int k = 0; k < 16; ++k) {
+            float a, d;
+            unpair(fma2(pair(sv[32 * c + 2 * k], sv[32 * c + 2 * k + 1]), sc, rf), a, d);
+            a = tc::ex2_ftz(a);
+            d = tc::ex2_ftz(d);
+            sum[k & 1] = add2(sum[k & 1], pair(a, d));
+            pk[k] = pack2(a, d);
           }
-        };
-        if (j0 + kBK > clear) probabilities(std::false_type{});
-        else probabilities(std::true_type{});
+          tc::tmem_st16(tS + 16 * c, pk);
+          if (c == 1 && !zero) {             // the first half of P V can start
+            tc::tmem_wait_st();
+            hand_over(&bar->p_half[w]);
+          }
+        }
         float s0, s1;
         unpair(add2(sum[0], sum[1]), s0, s1);
         l = l * factor + (s0 + s1);
