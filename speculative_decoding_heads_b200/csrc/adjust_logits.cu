@@ -4,10 +4,14 @@
 // A block owns kChunk tokens of one sequence's vocabulary.  It counts the
 // history's tokens of its chunk in shared memory (one word per token: bit 31
 // the token is in the prompt, the low bits its generated occurrences), sums
-// the biases, and then streams the chunk of every node of its group, a warp
-// per piece of a node's row.  The tokens on a node's own path (at most 17)
-// differ from node to node: a lane per path token recomputes that token from
-// the logit it read before the warp wrote the piece, and overwrites it.
+// the biases, lists the path tokens of its nodes, and turns the counts into
+// one addend per token (bias less penalties) and one bit (it occurred), so
+// that a logit costs z -> z m + addend with m one of 1, 1/repetition and
+// repetition.  Then it streams the chunk of every node of its group, a warp
+// per piece of a node's row.  The tokens on
+// a node's own path (at most 17) differ from node to node: a lane per path
+// token recomputes that token from the logit as it was before the warp wrote
+// the piece, and overwrites it.
 //
 // Bound by HBM: 8 bytes per logit; the history is read once per block, from L2.
 #include "common.cuh"
@@ -18,7 +22,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kChunk = 2048;                  // tokens per block
-constexpr int kPiece = 512;                   // tokens a warp streams at a time: 16 per lane
+constexpr int kPiece = 512;                   // tokens a warp streams at a time: 16 per lane, all loads in flight
+constexpr int kPath = MEDUSA_MAX_K + 1;       // nodes on a path
 constexpr uint32_t kPrompt = 0x80000000u;
 
 struct LogitArgs {
@@ -31,84 +36,80 @@ struct LogitArgs {
   int* status;
 };
 
+// 1/repetition is rounded once per block: a division per logit cost more than
+// the logit's traffic (88 us against 34 for 49 nodes of 16 sequences of 32003).
 struct Penalty {
-  float rep, pres, freq;
+  float rep, inv, pres, freq;
 };
 
-__device__ __forceinline__ float penalise(float z, uint32_t count, const Penalty& p) {
-  if (count != 0u) z = z > 0.f ? z / p.rep : z * p.rep;
+// What is added to a token's logit apart from the repetition penalty.
+__device__ __forceinline__ float addend(uint32_t count, float bias, const Penalty& p) {
   const uint32_t made = count & ~kPrompt;
-  if (made != 0u) z -= p.freq * static_cast<float>(made) + p.pres;
-  return z;
+  return made != 0u ? bias - fmaf(p.freq, static_cast<float>(made), p.pres) : bias;
+}
+__device__ __forceinline__ float adjust(float z, bool occurred, float add, const Penalty& p) {
+  const float m = occurred ? (z > 0.f ? p.inv : p.rep) : 1.f;
+  return fmaf(z, m, add);
 }
 
-// Tokens [v, v + 4) of a piece, aligned (kVec) or one token.
-template <bool kVec, bool kBias, bool kMask>
-__device__ __forceinline__ void stream_piece(const float* z, float* o, const uint32_t* allowed, const uint32_t* count,
-                                             const float* bias, int v0, int v1, int lane, const Penalty& pen) {
-  if constexpr (kVec) {
-    float4 x[kPiece / 128];
-#pragma unroll
-    for (int u = 0; u < kPiece / 128; ++u) {
-      const int v = v0 + u * 128 + 4 * lane;
-      if (v < v1) x[u] = *reinterpret_cast<const float4*>(z + v);
+// Node of the l-th set bit of an ancestor-mask row, -1 past the last.
+__device__ __forceinline__ int nth_ancestor(const uint64_t* anc, int words, int l) {
+  for (int w = 0; w < words; ++w) {
+    uint64_t x = anc[w];
+    const int c = __popcll(x);
+    if (l < c) {
+      for (; l > 0; --l) x &= x - 1;
+      return 64 * w + __ffsll(static_cast<long long>(x)) - 1;
     }
-#pragma unroll
-    for (int u = 0; u < kPiece / 128; ++u) {
-      const int v = v0 + u * 128 + 4 * lane;
-      if (v >= v1) continue;
-      const uint4 c = *reinterpret_cast<const uint4*>(count + (v & (kChunk - 1)));
-      if ((c.x | c.y | c.z | c.w) != 0u) {
-        x[u].x = penalise(x[u].x, c.x, pen);
-        x[u].y = penalise(x[u].y, c.y, pen);
-        x[u].z = penalise(x[u].z, c.z, pen);
-        x[u].w = penalise(x[u].w, c.w, pen);
-      }
-      if constexpr (kBias) {
-        const float4 w = *reinterpret_cast<const float4*>(bias + (v & (kChunk - 1)));
-        x[u].x += w.x;
-        x[u].y += w.y;
-        x[u].z += w.z;
-        x[u].w += w.w;
-      }
-      if constexpr (kMask) {
-        const uint32_t m = allowed[v >> 5] >> (v & 31);
-        if (!(m & 1u)) x[u].x = -INFINITY;
-        if (!(m & 2u)) x[u].y = -INFINITY;
-        if (!(m & 4u)) x[u].z = -INFINITY;
-        if (!(m & 8u)) x[u].w = -INFINITY;
-      }
-      *reinterpret_cast<float4*>(o + v) = x[u];
-    }
-  } else {
-    float x[kPiece / 32];
-#pragma unroll
-    for (int u = 0; u < kPiece / 32; ++u) {
-      const int v = v0 + u * 32 + lane;
-      if (v < v1) x[u] = z[v];
-    }
-#pragma unroll
-    for (int u = 0; u < kPiece / 32; ++u) {
-      const int v = v0 + u * 32 + lane;
-      if (v >= v1) continue;
-      x[u] = penalise(x[u], count[v & (kChunk - 1)], pen);
-      if constexpr (kBias) x[u] += bias[v & (kChunk - 1)];
-      if constexpr (kMask) {
-        if (!((allowed[v >> 5] >> (v & 31)) & 1u)) x[u] = -INFINITY;
-      }
-      o[v] = x[u];
-    }
+    l -= c;
   }
+  return -1;
 }
 
 template <bool kVec, bool kBias, bool kMask>
-__global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) adjust_logits_kernel(const LogitArgs a) {
   __shared__ __align__(16) uint32_t count[kChunk];
-  __shared__ __align__(16) float bias[kBias ? kChunk : 4];
+  __shared__ __align__(16) float add[kChunk];
+  __shared__ uint32_t occurred[kChunk / 32];
+  __shared__ float bias[kBias ? kChunk : 1];
+  __shared__ int32_t bias_ids[kBias ? MEDUSA_MAX_BIAS : 1];
+  extern __shared__ int32_t paths[];          // [nodes of the group][kPath] tokens, -1 past a path's end
   const int b = blockIdx.z, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int c0 = blockIdx.x * kChunk, c1 = min(c0 + kChunk, a.V);
   const int T = a.t.T;
   const bool penalties = a.r.repetition || a.r.presence || a.r.frequency;
+  const int node0 = static_cast<int>(static_cast<long long>(T) * blockIdx.y / a.groups);
+  const int node1 = static_cast<int>(static_cast<long long>(T) * (blockIdx.y + 1) / a.groups);
+
+  const int pieces = (c1 - c0 + kPiece - 1) / kPiece, total = (node1 - node0) * pieces;
+  float x[kPiece / 32];
+  auto load = [&](const float* z, int v0, int v1) {
+    if constexpr (kVec) {
+#pragma unroll
+      for (int k = 0; k < kPiece / 128; ++k) {
+        const int v = v0 + k * 128 + 4 * lane;
+        if (v < v1) *reinterpret_cast<float4*>(x + 4 * k) = *reinterpret_cast<const float4*>(z + v);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPiece / 32; ++k) {
+        const int v = v0 + k * 32 + lane;
+        if (v < v1) x[k] = z[v];
+      }
+    }
+  };
+  // Piece u of the group: node n of it, tokens [v0, v1).
+  auto piece = [&](int u, int& n, int& v0, int& v1) {
+    n = u / pieces;
+    v0 = c0 + (u - n * pieces) * kPiece;
+    v1 = min(v0 + kPiece, c1);
+  };
+  // The first piece is loaded while the block sets up.
+  int n, v0, v1;
+  if (warp < total) {
+    piece(warp, n, v0, v1);
+    load(a.logits + (static_cast<size_t>(b) * T + node0 + n) * a.V, v0, v1);
+  }
 
   int hist = 0, prompt = 0;
   if (a.r.history) {
@@ -123,77 +124,124 @@ __global__ void __launch_bounds__(kThreads) adjust_logits_kernel(const LogitArgs
     count[i] = 0u;
     if constexpr (kBias) bias[i] = 0.f;
   }
-  __syncthreads();
-  Penalty pen{1.f, 0.f, 0.f};
+  const int n_bias = kBias ? a.r.n_bias : 0;
+  if constexpr (kBias)
+    for (int i = tid; i < n_bias; i += kThreads) bias_ids[i] = a.r.bias_ids[static_cast<size_t>(b) * n_bias + i];
+  Penalty pen{1.f, 1.f, 0.f, 0.f};
   if (penalties) {
     if (a.r.repetition) pen.rep = a.r.repetition[b];
+    pen.inv = 1.f / pen.rep;
     if (a.r.presence) pen.pres = a.r.presence[b];
     if (a.r.frequency) pen.freq = a.r.frequency[b];
-    if (a.r.history) {
-      const int32_t* h = a.r.history + static_cast<size_t>(b) * a.r.history_cap;
-#pragma unroll 8
-      for (int i = tid; i < hist; i += kThreads) {
-        const int v = h[i];
-        if (v >= c0 && v < c1) {
-          if (i < prompt) atomicOr(&count[v - c0], kPrompt);
-          else atomicAdd(&count[v - c0], 1u);
-        }
+    for (int i = tid; i < (node1 - node0) * kPath; i += kThreads) {
+      const int k = i / kPath, l = i - k * kPath;
+      const int node = nth_ancestor(a.t.anc + static_cast<size_t>(node0 + k) * a.t.W, a.t.W, l);
+      paths[i] = node < 0 ? -1 : a.tokens[static_cast<size_t>(b) * T + node];
+    }
+  }
+  __syncthreads();
+  if (penalties && hist > 0) {
+    const int32_t* h = a.r.history + static_cast<size_t>(b) * a.r.history_cap;
+    auto note = [&](int v, int i) {
+      if (v >= c0 && v < c1) {
+        if (i < prompt) atomicOr(&count[v - c0], kPrompt);
+        else atomicAdd(&count[v - c0], 1u);
       }
+    };
+    // 16-byte loads between the first and the last aligned entry.
+    const int head = min(hist, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(h) & 15u)) & 15u) / 4);
+    const int quads = (hist - head) / 4;
+    if (tid < head) note(h[tid], tid);
+    const int tail = head + 4 * quads + tid;
+    if (tail < hist) note(h[tail], tail);
+    const int4* h4 = reinterpret_cast<const int4*>(h + head);
+#pragma unroll 4
+    for (int i = tid; i < quads; i += kThreads) {
+      const int4 v = h4[i];
+      note(v.x, head + 4 * i);
+      note(v.y, head + 4 * i + 1);
+      note(v.z, head + 4 * i + 2);
+      note(v.w, head + 4 * i + 3);
     }
   }
   if constexpr (kBias) {
     // A repeated id's values are added in list order by its first entry.
-    const int32_t* ids = a.r.bias_ids + static_cast<size_t>(b) * a.r.n_bias;
-    const float* val = a.r.bias + static_cast<size_t>(b) * a.r.n_bias;
-    for (int i = tid; i < a.r.n_bias; i += kThreads) {
-      const int v = ids[i];
+    const float* val = a.r.bias + static_cast<size_t>(b) * n_bias;
+    for (int i = tid; i < n_bias; i += kThreads) {
+      const int v = bias_ids[i];
       if (v < c0 || v >= c1) continue;
       bool first = true;
-      for (int k = 0; k < i && first; ++k) first = ids[k] != v;
+      for (int k = 0; k < i && first; ++k) first = bias_ids[k] != v;
       if (!first) continue;
       float s = val[i];
-      for (int k = i + 1; k < a.r.n_bias; ++k)
-        if (ids[k] == v) s += val[k];
+      for (int k = i + 1; k < n_bias; ++k)
+        if (bias_ids[k] == v) s += val[k];
       bias[v - c0] = s;
     }
   }
   __syncthreads();
+  for (int i = tid; i < kChunk; i += kThreads) {
+    add[i] = addend(count[i], kBias ? bias[i] : 0.f, pen);
+    const uint32_t bits = __ballot_sync(0xffffffffu, count[i] != 0u);
+    if (lane == 0) occurred[i >> 5] = bits;
+  }
+  __syncthreads();
 
-  const int pieces = (c1 - c0 + kPiece - 1) / kPiece;
-  const int node0 = static_cast<int>(static_cast<long long>(T) * blockIdx.y / a.groups);
-  const int node1 = static_cast<int>(static_cast<long long>(T) * (blockIdx.y + 1) / a.groups);
-  for (int u = warp; u < (node1 - node0) * pieces; u += kWarps) {
-    const int i = node0 + u / pieces, v0 = c0 + (u % pieces) * kPiece, v1 = min(v0 + kPiece, c1);
-    const size_t row = (static_cast<size_t>(b) * T + i);
+  for (int u = warp; u < total; u += kWarps) {
+    piece(u, n, v0, v1);
+    const size_t row = static_cast<size_t>(b) * T + node0 + n;
     const float* z = a.logits + row * a.V;
     float* o = a.out + row * a.V;
     const uint32_t* allowed = kMask ? a.r.allowed + row * a.words : nullptr;
-    // Lane l holds the path's node l steps above i, if any.
+    if (u != warp) load(z, v0, v1);
+    // Lane l's path token, if it lies in this piece, with its count on the path.
     int mine = -1;
     float fixed = 0.f;
     if (penalties) {
-      int node = i;
-      const int up = a.t.depth[i];
-      for (int l = 0; l <= up; ++l) {
-        if (l == lane) mine = a.tokens[static_cast<size_t>(b) * T + node];
-        node = a.t.parent[node];
-      }
-      const bool here = mine >= v0 && mine < v1;
-      if (!here) mine = -1;
-      if (__any_sync(0xffffffffu, here)) {
-        uint32_t more = 0u;
-        for (int l = 0; l <= up; ++l) more += __shfl_sync(0xffffffffu, mine, l) == mine;
-        if (here) {
-          fixed = penalise(z[mine], count[mine - c0] + more, pen);
-          if constexpr (kBias) fixed += bias[mine - c0];
-          if constexpr (kMask) {
-            if (!((allowed[mine >> 5] >> (mine & 31)) & 1u)) fixed = -INFINITY;
-          }
+      if (lane < kPath) mine = paths[n * kPath + lane];
+      if (mine < v0 || mine >= v1) mine = -1;
+      const uint32_t same = __match_any_sync(0xffffffffu, mine);
+      if (mine >= 0) {
+        fixed = adjust(z[mine], true, addend(count[mine - c0] + __popc(same), kBias ? bias[mine - c0] : 0.f, pen), pen);
+        if constexpr (kMask) {
+          if (!((allowed[mine >> 5] >> (mine & 31)) & 1u)) fixed = -INFINITY;
         }
       }
       __syncwarp();            // the reads above before the writes below (out may be logits)
     }
-    stream_piece<kVec, kBias, kMask>(z, o, allowed, count, bias, v0, v1, lane, pen);
+    if constexpr (kVec) {
+#pragma unroll
+      for (int k = 0; k < kPiece / 128; ++k) {
+        const int v = v0 + k * 128 + 4 * lane;
+        if (v >= v1) continue;
+        float4 y = *reinterpret_cast<float4*>(x + 4 * k);
+        const float4 w = *reinterpret_cast<const float4*>(add + (v - c0));
+        const uint32_t c = occurred[(v - c0) >> 5] >> (v & 31);
+        y.x = adjust(y.x, c & 1u, w.x, pen);
+        y.y = adjust(y.y, c & 2u, w.y, pen);
+        y.z = adjust(y.z, c & 4u, w.z, pen);
+        y.w = adjust(y.w, c & 8u, w.w, pen);
+        if constexpr (kMask) {
+          const uint32_t m = allowed[v >> 5] >> (v & 31);
+          if (!(m & 1u)) y.x = -INFINITY;
+          if (!(m & 2u)) y.y = -INFINITY;
+          if (!(m & 4u)) y.z = -INFINITY;
+          if (!(m & 8u)) y.w = -INFINITY;
+        }
+        *reinterpret_cast<float4*>(o + v) = y;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kPiece / 32; ++k) {
+        const int v = v0 + k * 32 + lane;
+        if (v >= v1) continue;
+        float y = adjust(x[k], occurred[(v - c0) >> 5] >> (v & 31) & 1u, add[v - c0], pen);
+        if constexpr (kMask) {
+          if (!((allowed[v >> 5] >> (v & 31)) & 1u)) y = -INFINITY;
+        }
+        o[v] = y;
+      }
+    }
     if (penalties) {
       __syncwarp();
       if (mine >= 0) o[mine] = fixed;   // lanes with the same token write the same value
@@ -215,16 +263,18 @@ medusa_status_t launch_adjust_logits(const TreeDev& t, int B, int V, const float
   a.out = out;
   a.status = device_status_ptr();
   const int chunks = (V + kChunk - 1) / kChunk;
-  // Node groups until the launch has about four blocks per SM, each with at
-  // least eight nodes (a block's set-up scans the whole history).
+  // Node groups until the launch fills the four blocks that an SM holds, once
+  // (a block's set-up scans the whole history), each with a piece for every
+  // warp.
   const long long base = static_cast<long long>(chunks) * B;
-  const int want = static_cast<int>((4ll * sm_count() + base - 1) / base);
-  const int most = t.T / 8 < 1 ? 1 : t.T / 8;
-  a.groups = want < 1 ? 1 : want > most ? most : want;
+  const long long want = 4ll * sm_count() / base < 1 ? 1 : 4ll * sm_count() / base;
+  const int most = t.T * (kChunk / kPiece) / kWarps < 1 ? 1 : t.T * (kChunk / kPiece) / kWarps;
+  a.groups = want > most ? most : static_cast<int>(want);
   const dim3 grid(chunks, a.groups, B);
+  const size_t smem = static_cast<size_t>((t.T + a.groups - 1) / a.groups) * kPath * sizeof(int32_t);   // at most 17 KB
   const bool vec = V % 4 == 0 && ((reinterpret_cast<uintptr_t>(logits) | reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
   const bool bias = rules.bias != nullptr, mask = rules.allowed != nullptr;
-  auto go = [&](auto kernel) { kernel<<<grid, kThreads, 0, stream>>>(a); };
+  auto go = [&](auto kernel) { kernel<<<grid, kThreads, smem, stream>>>(a); };
   if (vec) {
     if (bias) mask ? go(adjust_logits_kernel<true, true, true>) : go(adjust_logits_kernel<true, true, false>);
     else mask ? go(adjust_logits_kernel<true, false, true>) : go(adjust_logits_kernel<true, false, false>);

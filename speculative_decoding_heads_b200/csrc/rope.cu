@@ -15,8 +15,8 @@ namespace medusa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxTok = 8;      // tokens per block
-constexpr int kBatch = 4;       // heads a thread loads before it stores any
+constexpr int kMaxTok = 32;     // tokens per block
+constexpr int kBatch = 1;       // tokens a thread loads before it stores any
 
 struct RopeArgs {
   PagedDev kv;
@@ -107,7 +107,7 @@ struct Vec16<uint16_t> {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      u[i] = static_cast<uint32_t>(f32_to_bf16_rne(f[2 * i])) | (static_cast<uint32_t>(f32_to_bf16_rne(f[2 * i + 1])) << 16);
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u[i]) : "f"(f[2 * i + 1]), "f"(f[2 * i]));
     return make_uint4(u[0], u[1], u[2], u[3]);
   }
 };
@@ -147,79 +147,108 @@ __device__ int prepare_tokens(const RopeArgs& a, int n0, Place* place, float2* c
   return count;
 }
 
-// 16-byte path: a thread owns vector j of a head (in the half layout also its
-// partner rot/2 further on) and walks the heads of a token.
+// 16-byte path: a thread owns vector j of one head (in the half layout also
+// its partner rot/2 further on) and walks the block's tokens, kBatch of them
+// with all loads in flight, so that addresses advance by constant strides and
+// a head's kind is decided once.  Narrow models put several tokens side by
+// side, wide ones sweep over their heads (one sweep per blockIdx.y when there
+// are few tokens).
 template <typename T>
-__global__ void __launch_bounds__(kThreads) rope_append_vec(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) rope_append_vec(const RopeArgs a) {
   constexpr int E = Vec16<T>::kE;
-  extern __shared__ float2 cs[];
+  extern __shared__ __align__(16) float2 cs[];
   __shared__ Place place[kMaxTok];
-  const int n0 = blockIdx.x * a.tok;
-  const int count = prepare_tokens<T>(a, n0, place, cs);
-  const int hd = a.kv.hd, H = a.H, Hkv = a.kv.Hkv;
-  const int turned = a.half ? (a.rot >> 1) / E : a.rot / E;   // units that rotate
+  const int n0 = blockIdx.x * a.tok, count = min(a.tok, a.N - n0);
+  const int hd = a.kv.hd, H = a.H, Hkv = a.kv.Hkv, pairs = a.rot >> 1;
+  const int turned = a.half ? pairs / E : a.rot / E;          // units that rotate
   const int units = turned + (hd - a.rot) / E;
-  const int per = kThreads / units;                           // heads per sweep
-  const int h0 = threadIdx.x / units, j = threadIdx.x - h0 * units;
-  if (h0 >= per) return;
+  const int per = kThreads / units, heads = H + 2 * Hkv;      // heads per sweep
+  const int i0 = threadIdx.x / units, j = threadIdx.x - i0 * units;
+  const int side = per > heads ? per / heads : 1;             // tokens side by side
+  const int t0 = side > 1 ? i0 / heads : 0;
+  const bool idle = i0 >= per || t0 >= side;
   const bool two = a.half && j < turned;
   const int va = j < turned ? j * E : a.rot + (j - turned) * E;   // element offset of the (first) vector
-  const int vb = va + (a.rot >> 1);
-  const int heads = H + 2 * Hkv;
-  const long long page_head = static_cast<long long>(hd) << a.kv.page_shift;
-  for (int t = 0; t < count; ++t) {
-    const long long base = place[t].base;
-    if (base < 0) continue;
-    const long long n = n0 + t;
-    const float2* tcs = cs + t * (a.rot >> 1);
-    for (int hb = h0; hb < heads; hb += kBatch * per) {
-      uint4 x[kBatch], y[kBatch];
+  struct Step {                                               // kBatch tokens of one head
+    int h, tb, kind, hk;                                      // q, k or v, and the head in it
+    uint4 x[kBatch], y[kBatch];
+  };
+  auto load = [&](Step& s) {
+    s.kind = s.h < H ? 0 : s.h < H + Hkv ? 1 : 2;
+    s.hk = s.kind == 0 ? s.h : s.kind == 1 ? s.h - H : s.h - H - Hkv;
+    const long long step = s.kind == 0 ? a.qs : s.kind == 1 ? a.ks : a.vs;
+    const T* src = static_cast<const T*>(s.kind == 0 ? a.q : s.kind == 1 ? a.k : a.v) + (n0 + s.tb) * step + s.hk * hd + va;
 #pragma unroll
-      for (int m = 0; m < kBatch; ++m) {
-        const int h = hb + m * per;
-        if (h >= heads) continue;
-        const T* src = h < H ? static_cast<const T*>(a.q) + n * a.qs + static_cast<long long>(h) * hd
-                       : h < H + Hkv ? static_cast<const T*>(a.k) + n * a.ks + static_cast<long long>(h - H) * hd
-                                     : static_cast<const T*>(a.v) + n * a.vs + static_cast<long long>(h - H - Hkv) * hd;
-        x[m] = *reinterpret_cast<const uint4*>(src + va);
-        if (two) y[m] = *reinterpret_cast<const uint4*>(src + vb);
-      }
-#pragma unroll
-      for (int m = 0; m < kBatch; ++m) {
-        const int h = hb + m * per;
-        if (h >= heads) continue;
-        T* dst = h < H ? static_cast<T*>(a.q_out) + (n * H + h) * hd
-                 : h < H + Hkv ? static_cast<T*>(a.kv.k) + base + (h - H) * page_head
-                               : static_cast<T*>(a.kv.v) + base + (h - H - Hkv) * page_head;
-        if (j < turned && h < H + Hkv) {
-          float f[E];
-          Vec16<T>::unpack(x[m], f);
-          if (two) {
-            float g[E];
-            Vec16<T>::unpack(y[m], g);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-              const float2 w = tcs[va + e];
-              const float p = f[e] * w.x - g[e] * w.y, r = g[e] * w.x + f[e] * w.y;
-              f[e] = p;
-              g[e] = r;
-            }
-            y[m] = Vec16<T>::pack(g);
-          } else {
-#pragma unroll
-            for (int e = 0; e < E; e += 2) {
-              const float2 w = tcs[(va + e) >> 1];
-              const float p = f[e] * w.x - f[e + 1] * w.y, r = f[e + 1] * w.x + f[e] * w.y;
-              f[e] = p;
-              f[e + 1] = r;
-            }
-          }
-          x[m] = Vec16<T>::pack(f);
-        }
-        *reinterpret_cast<uint4*>(dst + va) = x[m];
-        if (two) *reinterpret_cast<uint4*>(dst + vb) = y[m];
-      }
+    for (int m = 0; m < kBatch; ++m) {
+      if (s.tb + m * side >= count) continue;
+      s.x[m] = *reinterpret_cast<const uint4*>(src + m * side * step);
+      if (two) s.y[m] = *reinterpret_cast<const uint4*>(src + m * side * step + pairs);
     }
+  };
+  auto follow = [&](const Step& s, Step& next) {              // false: s was the last
+    next.h = s.h;
+    next.tb = s.tb + kBatch * side;
+    if (next.tb >= count) {
+      next.tb = t0;
+      next.h += gridDim.y * per;
+    }
+    return next.h < heads;
+  };
+  auto finish = [&](Step& s) {
+    T* dst = s.kind == 0 ? static_cast<T*>(a.q_out) + (static_cast<long long>(n0) * H + s.hk) * hd + va
+                         : static_cast<T*>(s.kind == 1 ? a.kv.k : a.kv.v) + (static_cast<long long>(s.hk) * hd << a.kv.page_shift) + va;
+#pragma unroll
+    for (int m = 0; m < kBatch; ++m) {
+      const int t = s.tb + m * side;
+      if (t >= count || place[t].base < 0) continue;
+      if (j < turned && s.kind < 2) {
+        const float2* w = cs + t * pairs + (a.half ? va : va >> 1);
+        float f[E];
+        Vec16<T>::unpack(s.x[m], f);
+        if (two) {
+          float g[E];
+          Vec16<T>::unpack(s.y[m], g);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            const float p = f[e] * w[e].x - g[e] * w[e].y, r = g[e] * w[e].x + f[e] * w[e].y;
+            f[e] = p;
+            g[e] = r;
+          }
+          s.y[m] = Vec16<T>::pack(g);
+        } else {
+#pragma unroll
+          for (int e = 0; e < E / 2; ++e) {
+            const float p = f[2 * e] * w[e].x - f[2 * e + 1] * w[e].y, r = f[2 * e + 1] * w[e].x + f[2 * e] * w[e].y;
+            f[2 * e] = p;
+            f[2 * e + 1] = r;
+          }
+        }
+        s.x[m] = Vec16<T>::pack(f);
+      }
+      T* to = dst + (s.kind == 0 ? static_cast<long long>(t) * H * hd : place[t].base);
+      *reinterpret_cast<uint4*>(to) = s.x[m];
+      if (two) *reinterpret_cast<uint4*>(to + pairs) = s.y[m];
+    }
+  };
+  // The first loads wait for nothing: they run while the places and angles are
+  // worked out; later ones run while the step before is turned and stored
+  // (every vector is read before it is written, also when q_out is q).
+  Step s0, s1;
+  s0.h = i0 - t0 * heads + blockIdx.y * per;
+  s0.tb = t0;
+  const bool some = !idle && s0.h < heads && s0.tb < count;
+  if (some) load(s0);
+  prepare_tokens<T>(a, n0, place, cs);
+  if (!some) return;
+  for (;;) {
+    const bool more = follow(s0, s1);
+    if (more) load(s1);
+    finish(s0);
+    if (!more) return;
+    const bool again = follow(s1, s0);
+    if (again) load(s0);
+    finish(s1);
+    if (!again) return;
   }
 }
 
@@ -287,17 +316,21 @@ medusa_status_t launch_rope_append(const PagedDev& kv, medusa_dtype_t dtype, int
   a.positions = positions;
   a.starts = starts;
   a.status = device_status_ptr();
-  const int blocks = 4 * sm_count();
-  a.tok = N / blocks < 1 ? 1 : N / blocks > kMaxTok ? kMaxTok : N / blocks;
+  // Tokens per block: as many as give every SM its six blocks once (a second
+  // wave that is not full left a quarter of the SMs' time unused), up to 32.
+  const int es = dtype == MEDUSA_BF16 ? 2 : 4, slots = 6 * sm_count();
+  a.tok = (N + slots - 1) / slots < kMaxTok ? (N + slots - 1) / slots : kMaxTok;
   const int grid = (N + a.tok - 1) / a.tok;
-  const size_t smem = static_cast<size_t>(a.tok) * (a.rot / 2) * sizeof(float2);   // at most 8 KB
-  const int E = dtype == MEDUSA_BF16 ? 8 : 4;
+  const size_t smem = static_cast<size_t>(a.tok) * (a.rot / 2) * sizeof(float2);   // at most 32 KB
+  const int E = 16 / es;
   const bool vec = (a.half ? a.rot / 2 : a.rot) % E == 0;
+  const int turned = a.half ? a.rot / 2 / E : a.rot / E, per = vec ? kThreads / (turned + (kv.hd - a.rot) / E) : 1;
+  const int sweeps = N <= 2 * sm_count() ? (H + 2 * kv.Hkv + per - 1) / per : 1;
   if (dtype == MEDUSA_BF16) {
-    if (vec) rope_append_vec<uint16_t><<<grid, kThreads, smem, stream>>>(a);
+    if (vec) rope_append_vec<uint16_t><<<dim3(grid, sweeps), kThreads, smem, stream>>>(a);
     else rope_append_any<uint16_t><<<grid, kThreads, smem, stream>>>(a);
   } else {
-    if (vec) rope_append_vec<float><<<grid, kThreads, smem, stream>>>(a);
+    if (vec) rope_append_vec<float><<<dim3(grid, sweeps), kThreads, smem, stream>>>(a);
     else rope_append_any<float><<<grid, kThreads, smem, stream>>>(a);
   }
   const cudaError_t e = cudaGetLastError();
