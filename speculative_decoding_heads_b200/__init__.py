@@ -678,7 +678,7 @@ def medusa_generate(tree: Tree, model: Decoder, W1, b1, Wout, prompt, n_new: int
 def _arg(name: str, t, shape: tuple, dtype: torch.dtype, dev: int) -> int:
     """Device pointer of a contiguous tensor of this shape and dtype on device ``dev``; refusals as
     ``_spec`` and ``_p`` (a tensor on the host has device -1)."""
-    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
         _spec(name, t, shape, dtype)
     if t.get_device() != dev:
         _p(t)
@@ -688,7 +688,7 @@ def _arg(name: str, t, shape: tuple, dtype: torch.dtype, dev: int) -> int:
 def _device_of(t: torch.Tensor) -> int:
     """Index of the current device, which a CUDA tensor must be on; -1 (no device) for a host tensor,
     so that its call reports what else is wrong with its arguments first."""
-    return torch.cuda.current_device() if t.is_cuda else -1
+    return torch._C._cuda_getDevice() if t.is_cuda else -1
 
 
 def _stream_ptr(stream, dev: int) -> int:
@@ -752,21 +752,22 @@ def _on(t: torch.Tensor, dev: int):
 
 def _token_rows(name: str, t, N: int, heads: int, kv: "PagedKV", dev: int):
     """(pointer, token stride in elements) of a [N, heads, hd] tensor whose heads are dense."""
-    _require(isinstance(t, torch.Tensor) and t.shape == (N, heads, kv.hd), f"{name} must be [{N}, {heads}, {kv.hd}]")
-    _require(t.dtype == kv.dtype, f"{name} has dtype {t.dtype}, expected {kv.dtype}")
+    if not isinstance(t, torch.Tensor) or t.shape != (N, heads, kv.hd) or t.dtype != kv.dtype:
+        raise ValueError(f"{name} must be [{N}, {heads}, {kv.hd}] {kv.dtype}")
     s0, s1, s2 = t.stride()
-    _require(s2 == 1 and (s1 == kv.hd or heads == 1), f"the heads of a token of {name} must be dense")
+    if s2 != 1 or (s1 != kv.hd and heads != 1):
+        raise ValueError(f"the heads of a token of {name} must be dense")
     if t.get_device() != dev:
         _p(t)
     return t.data_ptr(), s0 if N > 1 else heads * kv.hd
 
 
 def _chunk_starts(kv: "PagedKV", N: int, chunk_starts, dev: int):
-    _require(N >= 1, "at least one token")
-    if chunk_starts is None:
-        _require(N % kv.B == 0, "without chunk_starts every sequence has N / B tokens")
-        return None
-    return _arg("chunk_starts", chunk_starts, (kv.B + 1,), torch.int32, dev)
+    if chunk_starts is not None:
+        return _arg("chunk_starts", chunk_starts, (kv.B + 1,), torch.int32, dev)
+    if N % kv.B != 0:
+        raise ValueError("without chunk_starts every sequence has N / B tokens")
+    return None
 
 
 def medusa_rope_append(kv: PagedKV, layer: int, q, k, v, q_out, rotary: Rotary, positions=None, chunk_starts=None,
@@ -775,7 +776,8 @@ def medusa_rope_append(kv: PagedKV, layer: int, q, k, v, q_out, rotary: Rotary, 
     next to it, at rows seq_lens[b] + i.  q, k and v may be slices of one fused product's output
     (any token stride of whole 16-byte units).  positions [N] int32: the rotation's positions, else
     the cache rows; chunk_starts [B+1] int32: ragged chunks, else N / B tokens each."""
-    _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be [N, H, hd]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] < 1:
+        raise ValueError("q must be [N, H, hd] with at least one token")
     N, H, _ = q.shape
     dev = _device_of(kv.k_pages)
     qp, qs = _token_rows("q", q, N, H, kv, dev)
@@ -800,16 +802,16 @@ def medusa_paged_attention(kv: PagedKV, layer: int, q, out, scale: float, ws, tr
     already holds their keys and values, into out [N, H, hd].  Without a tree token i of a sequence
     sees the prefix and the chunk's tokens up to itself; with one, the prefix, its ancestors and
     itself (N = B * tree.T)."""
-    _require(isinstance(q, torch.Tensor) and q.dim() == 3, "q must be [N, H, hd]")
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[0] < 1:
+        raise ValueError("q must be [N, H, hd] with at least one token")
     N, H, _ = q.shape
     dev = _device_of(kv.k_pages)
     shape = (N, H, kv.hd)
     qp = _arg("q", q, shape, kv.dtype, dev)
     op = _arg("out", out, shape, kv.dtype, dev)
     st = _chunk_starts(kv, N, chunk_starts, dev)
-    if tree is not None:
-        _require(N == kv.B * tree.T and chunk_starts is None,
-                 f"with a tree q must hold {tree.T} rows per sequence, and chunk_starts be absent")
+    if tree is not None and (N != kv.B * tree.T or chunk_starts is not None):
+        raise ValueError(f"with a tree q must hold {tree.T} rows per sequence, and chunk_starts be absent")
     nbytes = _nbytes("ws", ws)
     _on(kv.k_pages, dev)
     _on(ws, dev)
@@ -842,9 +844,11 @@ def medusa_adjust_logits(tree: Tree, logits, tree_tokens, out, history=None, his
     (which may be logits).  history [B, cap] int32 with history_lens and prompt_lens [B] (its leading
     prompt tokens count for the repetition penalty only); repetition, presence, frequency [B] fp32;
     bias_ids / bias [B, n]; allowed [B, T, ceil(V / 32)] int32, a bit per token."""
-    _require(isinstance(logits, torch.Tensor) and logits.dim() == 3, "logits must be [B, T, V]")
+    if not isinstance(logits, torch.Tensor) or logits.dim() != 3:
+        raise ValueError("logits must be [B, T, V]")
     B, T, V = logits.shape
-    _require(T == tree.T, f"logits hold {T} tree nodes per sequence; the tree has {tree.T}")
+    if T != tree.T:
+        raise ValueError(f"logits hold {T} tree nodes per sequence; the tree has {tree.T}")
     dev = _device_of(logits)
     i32, f32 = torch.int32, torch.float32
     zp = _arg("logits", logits, (B, T, V), f32, dev)
@@ -860,8 +864,8 @@ def medusa_adjust_logits(tree: Tree, logits, tree_tokens, out, history=None, his
     if frequency is not None:
         r.frequency = _arg("frequency", frequency, (B,), f32, dev)
     if history is not None:
-        _require(isinstance(history, torch.Tensor) and history.dim() == 2 and history.shape[1] >= 1,
-                 "history must be [B, cap]")
+        if not isinstance(history, torch.Tensor) or history.dim() != 2 or history.shape[1] < 1:
+            raise ValueError("history must be [B, cap]")
         cap = r.history_cap = history.shape[1]
         r.history = _arg("history", history, (B, cap), i32, dev)
         r.history_lens = _arg("history_lens", history_lens, (B,), i32, dev)
@@ -871,8 +875,8 @@ def medusa_adjust_logits(tree: Tree, logits, tree_tokens, out, history=None, his
         _require(history_lens is None and prompt_lens is None, "history_lens and prompt_lens need a history")
     _require((bias_ids is None) == (bias is None), "bias_ids and bias go together")
     if bias is not None:
-        _require(isinstance(bias_ids, torch.Tensor) and bias_ids.dim() == 2 and 1 <= bias_ids.shape[1] <= MAX_BIAS,
-                 f"bias_ids must be [B, n] with 1 <= n <= {MAX_BIAS}")
+        if not isinstance(bias_ids, torch.Tensor) or bias_ids.dim() != 2 or not 1 <= bias_ids.shape[1] <= MAX_BIAS:
+            raise ValueError(f"bias_ids must be [B, n] with 1 <= n <= {MAX_BIAS}")
         n = r.n_bias = bias_ids.shape[1]
         r.bias_ids = _arg("bias_ids", bias_ids, (B, n), i32, dev)
         r.bias = _arg("bias", bias, (B, n), f32, dev)

@@ -181,6 +181,13 @@ size_t paged_attention_tc_workspace_bytes(const PagedDev& kv, int N, int H);
 medusa_status_t launch_paged_attention_tc(const PagedDev& kv, int N, int H, const void* q, float scale,
                                           const TreeDev* tree, const int32_t* starts, void* out, void* ws,
                                           cudaStream_t stream);
+// Its kernel for few query rows (paged_attention_few.cu): bf16, hd 64 or 128,
+// at most 16 rows per sequence and key head.
+bool paged_attention_few_supported(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const int32_t* starts);
+size_t paged_attention_few_workspace_bytes(const PagedDev& kv, int N, int H);
+medusa_status_t launch_paged_attention_few(const PagedDev& kv, int N, int H, const void* q, float scale,
+                                           const TreeDev* tree, const int32_t* starts, void* out, void* ws,
+                                           cudaStream_t stream);
 medusa_status_t launch_paged_accept(const TreeDev& t, const PagedDev& kv, int layers, medusa_dtype_t dtype,
                                     const int32_t* best_path, const int32_t* accept_len, int32_t* new_lens, void* ws,
                                     cudaStream_t stream);

@@ -133,12 +133,20 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       for (int r = 0; r < RR; ++r) {
         const int rr = x.tile * R + ty * RR + r, tok = rr / g;
         float mx = -INFINITY;
+        // Nodes j0 - L .. of the tree that this row sees, one bit per key of the block.
+        uint64_t sees = 0ull;
+        if (w.t.T > 0 && j0 + kBK > L && tok < n) {
+          const int o = j0 - L, wi = o >= 0 ? o >> 6 : 0, sh = o >= 0 ? o & 63 : -o;
+          const uint64_t* a = w.t.anc + tok * w.t.W;
+          const uint64_t w0 = wi < w.t.W ? a[wi] : 0ull, w1 = wi + 1 < w.t.W ? a[wi + 1] : 0ull;
+          sees = o < 0 ? w0 << sh | ((1ull << sh) - 1ull) : sh == 0 ? w0 : (w0 >> sh) | (w1 << (64 - sh));
+        }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           const int j = j0 + tx + 16 * c, rel = j - L;
           bool see;
           if (w.t.T > 0)
-            see = rel < 0 || (rel < n && tok < n && ((w.t.anc[tok * w.t.W + (rel >> 6)] >> (rel & 63)) & 1ull));
+            see = rel < 0 || (rel < n && (sees >> (tx + 16 * c) & 1ull));
           else
             see = rel <= tok && rel < n;
           s[r][c] = see ? s[r][c] * scale_log2 : -INFINITY;
@@ -304,16 +312,22 @@ cudaError_t run_for(const Choice& c, const Work& w, int grid, const void* q, flo
 
 size_t paged_attention_workspace_bytes(const PagedDev& kv, medusa_dtype_t dtype, int N, int H) {
   const Choice c = choose(kv, N, H);
-  const size_t tc = paged_attention_tc_supported(kv, dtype, H) ? paged_attention_tc_workspace_bytes(kv, N, H) : 0;
+  size_t tc = paged_attention_tc_supported(kv, dtype, H) ? paged_attention_tc_workspace_bytes(kv, N, H) : 0;
+  if (paged_attention_few_supported(kv, dtype, N, H, nullptr)) {
+    const size_t few = paged_attention_few_workspace_bytes(kv, N, H);
+    tc = few > tc ? few : tc;
+  }
   const size_t any = counter_bytes(N, H, kv.Hkv, kv.B, c.R) +
          2ull * sm_count() * c.per_sm * slot_floats(c.R, c.HD) * sizeof(float);
-  return tc > any ? tc : any;      // the scale, known only at the call, decides between the two
+  return tc > any ? tc : any;      // the scale and the chunks, known only at the call, decide between them
 }
 
 medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const void* q,
                                        float scale, const TreeDev* tree, const int32_t* starts, void* out, void* ws,
                                        cudaStream_t stream) {
-  // The tensor-core kernel takes the maximum of the unscaled scores.
+  // These two take the maximum of the unscaled scores.
+  if (scale > 0.f && paged_attention_few_supported(kv, dtype, N, H, starts))
+    return launch_paged_attention_few(kv, N, H, q, scale, tree, starts, out, ws, stream);
   if (scale > 0.f && paged_attention_tc_supported(kv, dtype, H))
     return launch_paged_attention_tc(kv, N, H, q, scale, tree, starts, out, ws, stream);
   Work w{};
