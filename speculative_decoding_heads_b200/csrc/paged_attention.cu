@@ -8,7 +8,9 @@
 // A CTA holds R query rows and takes 64 keys at a time through shared memory
 // as fp32; a thread owns R / 16 or R / 8 rows x 4 keys of the scores and the
 // same rows x HD / 16 dimensions of O, so one 16-byte shared-memory read
-// feeds 16 products.  R = 16 where the largest chunk fits (decoding and small
+// feeds 16 products.  The probabilities take the place of the keys, which
+// leaves room for two CTAs per SM at 128 dimensions: one computes while the
+// other's loads are in flight.  R = 16 where the largest chunk fits (decoding and small
 // trees, bound by the cache's bytes), 64 otherwise (bound by fp32 arithmetic).
 #include "paged_work.cuh"
 
@@ -42,8 +44,12 @@ struct Shape {
   static constexpr int kThreads = R / kRows * 16;     // 16 threads side by side per row group
   static constexpr int kPitch = HD + 4;               // floats per row: conflict-free 16-byte reads down a column
   static constexpr int kPPitch = kBK + 4;
-  static constexpr size_t kSmem = (static_cast<size_t>(R + 2 * kBK) * kPitch + R * kPPitch) * sizeof(float);
-  static constexpr int kPerSm = kSmem > 110 * 1024 ? 1 : kSmem > 73 * 1024 ? 2 : 3;
+  static_assert(R * kPPitch <= kBK * kPitch, "the probabilities take the place of the keys");
+  static constexpr size_t kSmem = static_cast<size_t>(R + 2 * kBK) * kPitch * sizeof(float);
+  static constexpr int kPerSm = kSmem > 112 * 1024 ? 1 : kSmem > 74 * 1024 || R == 64 ? 2 : 3;
+  static constexpr int kLoads = kBK * (HD / 4) / kThreads;   // four-element loads of K, and of V, per thread and block
+  static constexpr int kBatch = kLoads < 8 ? kLoads : 8;     // in flight together
+  static_assert(kLoads % kBatch == 0 && kBK * (HD / 4) % kThreads == 0, "whole batches");
 };
 
 template <typename T, int HD, int R>
@@ -55,7 +61,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
   float* qs = sh;
   float* ks = qs + R * S::kPitch;
   float* vs = ks + kBK * S::kPitch;
-  float* ps = vs + kBK * S::kPitch;
+  float* ps = ks;
   __shared__ Plan plan;
   __shared__ int s_last;
   const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
@@ -93,22 +99,35 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
     for (int kb = x.kb0; kb < x.kb1; ++kb) {
       const int j0 = kb * kBK;
       __syncthreads();
-      for (int i = tid; i < kBK * (HD / 4); i += NT) {
-        const int r = i / (HD / 4), d = i - r * (HD / 4);
-        float4 kk = make_float4(0.f, 0.f, 0.f, 0.f), vv = kk;
-        if (j0 + r < keys && d < hd4) {    // rows past the sequence are not read
-          const int page = w.kv.table[static_cast<long long>(b) * w.kv.max_pages + ((j0 + r) >> shift)];
-          if (page >= 0 && page < w.kv.n_pages) {
-            const long long off =
-                (((static_cast<long long>(page) * w.kv.Hkv + x.h) << shift) + ((j0 + r) & mask)) * hd + 4 * d;
-            kk = load4<T>(static_cast<const T*>(w.kv.k) + off);
-            vv = load4<T>(static_cast<const T*>(w.kv.v) + off);
-          } else {
-            set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
+      // A batch's places first, then its loads together: one after the other
+      // they took as long as the products.
+#pragma unroll 1
+      for (int base = 0; base < S::kLoads; base += S::kBatch) {
+        long long off[S::kBatch];
+        float4 t[S::kBatch];
+#pragma unroll
+        for (int u = 0; u < S::kBatch; ++u) {
+          const int i = tid + (base + u) * NT, r = i / (HD / 4), d = i - r * (HD / 4);
+          off[u] = -1;
+          if (j0 + r < keys && d < hd4) {    // rows past the sequence are not read
+            const int page = w.kv.table[static_cast<long long>(b) * w.kv.max_pages + ((j0 + r) >> shift)];
+            if (page >= 0 && page < w.kv.n_pages)
+              off[u] = (((static_cast<long long>(page) * w.kv.Hkv + x.h) << shift) + ((j0 + r) & mask)) * hd + 4 * d;
+            else
+              set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
           }
         }
-        *reinterpret_cast<float4*>(ks + r * S::kPitch + 4 * d) = kk;
-        *reinterpret_cast<float4*>(vs + r * S::kPitch + 4 * d) = vv;
+        auto fetch = [&](const void* from, float* to) {
+#pragma unroll
+          for (int u = 0; u < S::kBatch; ++u) t[u] = off[u] >= 0 ? load4<T>(static_cast<const T*>(from) + off[u]) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < S::kBatch; ++u) {
+            const int i = tid + (base + u) * NT, r = i / (HD / 4), d = i - r * (HD / 4);
+            *reinterpret_cast<float4*>(to + r * S::kPitch + 4 * d) = t[u];
+          }
+        };
+        fetch(w.kv.k, ks);
+        fetch(w.kv.v, vs);
       }
       __syncthreads();
       float s[RR][4];
@@ -129,6 +148,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
           for (int c = 0; c < 4; ++c)
             s[r][c] = fmaf(a[r].x, k4[c].x, fmaf(a[r].y, k4[c].y, fmaf(a[r].z, k4[c].z, fmaf(a[r].w, k4[c].w, s[r][c]))));
       }
+      __syncthreads();                     // P goes where K was
 #pragma unroll
       for (int r = 0; r < RR; ++r) {
         const int rr = x.tile * R + ty * RR + r, tok = rr / g;
