@@ -2,8 +2,11 @@
 // pages: row L + j <- row L + n_j for j = 0..a, every layer and head, K and V.
 // A source can be the destination of a later j, so each thread owns one
 // 16-byte column of one head's K or V rows and loads all its sources before it
-// writes any.  A block first looks up the path's page offsets once, with one
-// thread per accepted row.
+// writes any (row 0 is the root and stays).  A block first looks up the path's
+// page offsets once, with one thread per accepted row.
+//
+// Bound by the latency of these dependent reads, so by how many threads are in
+// flight: the registers are those of the tree's own depth (4, 8 or 16 rows).
 //
 // new_lens may be the lengths that the blocks read: then the last block to
 // finish (a ticket in the workspace) writes it.
@@ -37,6 +40,8 @@ __device__ __forceinline__ int accepted(const AcceptArgs& a, int b, int* L, int*
   return a.t.retrieve[*best * (a.t.D + 1) + n] < 0 ? -1 : n;
 }
 
+// kRows: accepted rows below the root that a thread can hold.
+template <int kRows>
 __global__ void __launch_bounds__(kThreads) paged_accept_kernel(const AcceptArgs a) {
   __shared__ long long from[kMaxRows], to[kMaxRows];   // column offset of head 0, from < 0: nothing to move
   __shared__ int s_n;
@@ -72,13 +77,13 @@ __global__ void __launch_bounds__(kThreads) paged_accept_kernel(const AcceptArgs
     const int h = rem / a.chunks, c = rem - h * a.chunks;
     uint4* base = static_cast<uint4*>(which ? a.kv.v : a.kv.k) + layer * a.layer_stride +
                   (static_cast<long long>(h) << a.kv.page_shift) * a.chunks + c;
-    uint4 r[kMaxRows];
+    uint4 r[kRows];
 #pragma unroll
-    for (int j = 0; j < kMaxRows; ++j)
-      if (j <= n && from[j] >= 0) r[j] = base[from[j]];
+    for (int j = 0; j < kRows; ++j)
+      if (j < n && from[j + 1] >= 0) r[j] = base[from[j + 1]];
 #pragma unroll
-    for (int j = 0; j < kMaxRows; ++j)
-      if (j <= n && from[j] >= 0) base[to[j]] = r[j];
+    for (int j = 0; j < kRows; ++j)
+      if (j < n && from[j + 1] >= 0) base[to[j + 1]] = r[j];
   }
   if (a.ticket) {
     __shared__ unsigned s_last;
@@ -121,7 +126,9 @@ medusa_status_t launch_paged_accept(const TreeDev& t, const PagedDev& kv, int la
   a.ticket = new_lens == kv.lens ? static_cast<unsigned*>(ws) : nullptr;
   a.status = device_status_ptr();
   const dim3 grid((2 * kv.Hkv * a.chunks + kThreads - 1) / kThreads, kv.B, layers);
-  paged_accept_kernel<<<grid, kThreads, 0, stream>>>(a);
+  if (t.D <= 4) paged_accept_kernel<4><<<grid, kThreads, 0, stream>>>(a);
+  else if (t.D <= 8) paged_accept_kernel<8><<<grid, kThreads, 0, stream>>>(a);
+  else paged_accept_kernel<16><<<grid, kThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? MEDUSA_OK : cuda_fail("medusa_paged_accept_kv", e);
 }

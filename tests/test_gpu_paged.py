@@ -305,12 +305,17 @@ def test_paged_attention_shared_prefix(mb):
 # ---------------------------------------------------------------------------
 
 
+CHAIN = [(0,), (1,)] + [(1,) + (0,) * n for n in range(1, 16)]    # depth 16, every node one row behind its depth
+ACCEPT_TREES = {"d4": (4, 8, O.ranksum_choices(4, 8, 48)), "d5": (5, 10, O.ranksum_choices(5, 10, 63)), "d16": (16, 2, CHAIN)}
+
+
+@pytest.mark.parametrize("tree_of", sorted(ACCEPT_TREES))
 @pytest.mark.parametrize("dtype,hd,page,Hkv,lens,in_place", [
     ("bf16", 128, 16, 4, [0, 15, 33], True), ("bf16", 64, 8, 1, [7], False), ("f32", 64, 64, 3, [62, 1, 130, 64], True),
     ("f32", 8, 8, 2, [5, 2], False), ("bf16", 128, 256, 40, [250, 3], True)])
-def test_paged_accept(mb, dtype, hd, page, Hkv, lens, in_place):
-    choices = O.ranksum_choices(4, 8, 48)
-    tree = mb.Tree(choices, 4, 8)
+def test_paged_accept(mb, dtype, hd, page, Hkv, lens, in_place, tree_of):
+    K, topk, choices = ACCEPT_TREES[tree_of]
+    tree = mb.Tree(choices, K, topk)
     ret = tree.tables()["retrieve"]
     rng = np.random.default_rng(len(lens) + hd)
     ws = None
@@ -318,6 +323,9 @@ def test_paged_accept(mb, dtype, hd, page, Hkv, lens, in_place):
         c = Cache(mb, dtype, hd, page, Hkv, lens, [tree.T] * len(lens), layers=3, seed=trial)
         best = [int(rng.integers(tree.P)) for _ in lens]
         acc = [int(rng.integers(sum(x >= 0 for x in ret[p]))) for p in best]
+        if trial == 3:                            # the deepest path, all of it
+            best = [max(range(tree.P), key=lambda p: sum(x >= 0 for x in ret[p]))] * len(lens)
+            acc = [tree.D] * len(lens)
         want = [PO.accept(t.cpu().float().numpy(), c.table, lens, ret, best, acc) for t in (c.k, c.v)]
         ws = mb.workspace(mb.medusa_paged_accept_workspace_size(c.kv)) if ws is None else ws
         new = c.kv.seq_lens if in_place else torch.full_like(c.kv.seq_lens, -5)
