@@ -520,7 +520,10 @@ typedef struct medusa_paged_kv {
  * outside [0, N), a negative length, or seq_lens[b] + chunk > max_pages * page
  * sets MEDUSA_ERR_DEVICE_CHECK and leaves that sequence's rows unwritten, as
  * does a page id outside [0, n_pages) for the rows in that page (where
- * attention reads such a page, its keys and values count as zeros). */
+ * attention reads such a page, its keys and values count as zeros).
+ * chunk_starts that descend set it too, and attention then computes nothing;
+ * so does attention over more than 2^31 blocks of keys in one call.
+ * 1 <= N <= 2^22, 1 <= H <= 256. */
 
 typedef enum medusa_rope_layout {
   MEDUSA_ROPE_HALF = 0,          /* pair i of the rotated part: dimensions i and i + rot/2 */
@@ -570,8 +573,10 @@ medusa_status_t medusa_rope_append(const medusa_paged_kv_t* kv, int layer, int N
                                    const int32_t* positions, const int32_t* chunk_starts, cudaStream_t stream);
 
 /* Bytes for medusa_paged_attention with N query rows of H heads (0 on bad
- * arguments).  Zero-filled before its first use; two calls that may run at
- * the same time (two streams, two captured graphs) need one each. */
+ * arguments).  Zero-filled before its first use (and again after a call that
+ * reported MEDUSA_ERR_TIMEOUT); calls of any shapes that it is large enough
+ * for may use one workspace in turn, two calls that may run at the same time
+ * (two streams, two captured graphs) need one each. */
 size_t medusa_paged_attention_workspace_size(const medusa_paged_kv_t* kv, int N, int H);
 
 /* Attention of the new tokens over layer `layer` of the paged cache, their
@@ -583,15 +588,16 @@ size_t medusa_paged_attention_workspace_size(const medusa_paged_kv_t* kv, int N,
  *               chunk_starts must be NULL
  *   q, out [N, H, hd] contiguous in the cache's dtype, H a multiple of Hkv.
  * fp32 scores, softmax and accumulation; in bf16 the probabilities enter the
- * second product rounded to bf16 and the output is rounded once.  scale must
- * be finite.  Results do not depend on the order in which the GPU runs the
+ * second product rounded to bf16 and the output is rounded once.  |scale| is
+ * at most 2^64.  Results do not depend on the order in which the GPU runs the
  * blocks.  A non-finite value row of a NEW token can reach the other new rows
  * of its sequence (its weight there is zero, and 0 * inf is NaN). */
 medusa_status_t medusa_paged_attention(const medusa_paged_kv_t* kv, int layer, int N, int H, const void* q,
                                        float scale, const medusa_tree_t* tree, const int32_t* chunk_starts,
                                        void* out, void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes for medusa_paged_accept_kv. */
+/* Bytes for medusa_paged_accept_kv.  Zero-filled before its first use; two
+ * calls that may run at the same time need one each. */
 size_t medusa_paged_accept_workspace_size(const medusa_paged_kv_t* kv);
 
 /* medusa_accept_kv inside the pages: for every layer and head, with L =
@@ -641,7 +647,7 @@ typedef struct medusa_logit_rules {
  * outside [0, V) are skipped (padding).  history_lens[b] outside [0,
  * history_cap] or prompt_lens[b] < 0 sets MEDUSA_ERR_DEVICE_CHECK and leaves
  * that sequence's rows unwritten.
- *   logits, out [B, T, V] fp32; out may be logits.
+ *   logits, out [B, T, V] fp32, V <= 2^30; out may be logits.
  *   tree_tokens [B, T] int32, required with any of the three penalties.
  * No workspace.  ["Medusa API参考", evaluate_posterior: the logits it samples
  * from; the pages name no logit processing.] */

@@ -12,6 +12,8 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 constexpr int kMaxTokens = 1 << 22;   // packed rows of a call: row * heads stays inside 32 bits
 constexpr int kMaxHeads = 256;
+constexpr float kMaxScale = 18446744073709551616.f;   // 2^64: scale * log2(e) stays finite
+constexpr int kMaxVocab = 1 << 30;    // a chunk's end stays inside 31 bits
 
 medusa_status_t check_kv(const medusa_paged_kv_t* kv, const char* fn) {
   const std::string f(fn);
@@ -167,7 +169,7 @@ extern "C" medusa_status_t medusa_paged_attention(const medusa_paged_kv_t* kv, i
   if (st != MEDUSA_OK) return st;
   if (!q || !out || !workspace) return fail(MEDUSA_ERR_INVALID_ARG, f + ": null pointer");
   if (H % kv->Hkv != 0) return fail(MEDUSA_ERR_INVALID_ARG, f + ": H must be a multiple of Hkv");
-  if (!std::isfinite(scale)) return fail(MEDUSA_ERR_INVALID_ARG, f + ": scale must be finite");
+  if (!(std::fabs(scale) <= kMaxScale)) return fail(MEDUSA_ERR_INVALID_ARG, f + ": |scale| must be at most 2^64");
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 256))
     return fail(MEDUSA_ERR_INVALID_ARG, f + ": misaligned pointer");
   const size_t bytes = static_cast<size_t>(N) * H * kv->hd * element_bytes(kv->dtype);
@@ -221,7 +223,7 @@ extern "C" medusa_status_t medusa_adjust_logits(const medusa_tree_t* tree, int B
   const char* fn = "medusa_adjust_logits";
   const std::string f(fn);
   if (!logits || !out || !rules) return fail(MEDUSA_ERR_INVALID_ARG, f + ": null pointer");
-  if (B < 1 || B > MEDUSA_MAX_B || V < 1) return fail(MEDUSA_ERR_INVALID_ARG, f + ": B or V");
+  if (B < 1 || B > MEDUSA_MAX_B || V < 1 || V > kMaxVocab) return fail(MEDUSA_ERR_INVALID_ARG, f + ": B or V");
   const medusa_logit_rules_t& r = *rules;
   if ((r.history != nullptr) != (r.history_lens != nullptr) || (r.history && r.history_cap < 1) ||
       (r.prompt_lens && !r.history))

@@ -49,6 +49,7 @@ struct Shape {
   static constexpr int kPerSm = kSmem > 112 * 1024 ? 1 : kSmem > 74 * 1024 || R == 64 ? 2 : 3;
   static constexpr int kLoads = kBK * (HD / 4) / kThreads;   // four-element loads of K, and of V, per thread and block
   static constexpr int kBatch = kLoads < 8 ? kLoads : 8;     // in flight together
+  static_assert(2 * kPerSm * slot_floats(R, HD) <= kSlotFloatsPerSm, "two slots per CTA");
   static_assert(kLoads % kBatch == 0 && kBK * (HD / 4) % kThreads == 0, "whole batches");
 };
 
@@ -337,8 +338,7 @@ size_t paged_attention_workspace_bytes(const PagedDev& kv, medusa_dtype_t dtype,
     const size_t few = paged_attention_few_workspace_bytes(kv, N, H);
     tc = few > tc ? few : tc;
   }
-  const size_t any = counter_bytes(N, H, kv.Hkv, kv.B, c.R) +
-         2ull * sm_count() * c.per_sm * slot_floats(c.R, c.HD) * sizeof(float);
+  const size_t any = slots_bytes() + counter_bytes(N, H, kv.Hkv, kv.B, c.R);
   return tc > any ? tc : any;      // the scale and the chunks, known only at the call, decide between them
 }
 
@@ -360,8 +360,8 @@ medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype,
   w.status = device_status_ptr();
   const Choice c = choose(kv, N, H);
   w.R = c.R;
-  w.counters = static_cast<unsigned*>(ws);
-  w.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + counter_bytes(N, H, kv.Hkv, kv.B, c.R));
+  w.slots = static_cast<float*>(ws);
+  w.counters = counters_of(ws);
   const int grid = sm_count() * c.per_sm;
   const float s = scale * kLog2e;
   const cudaError_t e = dtype == MEDUSA_BF16 ? run_for<uint16_t>(c, w, grid, q, s, out, stream)

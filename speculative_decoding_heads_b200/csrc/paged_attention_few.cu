@@ -54,6 +54,7 @@ struct Bars {
 template <int HD>
 constexpr int smem_bytes() { return Shape<HD>::kOffBars + static_cast<int>(sizeof(Bars)); }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory budget");
+static_assert(2 * slot_floats(16, 128) <= kSlotFloatsPerSm, "two slots per CTA");
 
 struct Params {
   Work w;
@@ -535,8 +536,8 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.q = static_cast<const uint16_t*>(q);
   p.scale_log2 = scale * kLog2e;
   p.out = static_cast<uint16_t*>(out);
-  p.w.counters = static_cast<unsigned*>(ws);
-  p.w.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + counter_bytes(N, H, kv.Hkv, kv.B, S::kRows));
+  p.w.slots = static_cast<float*>(ws);
+  p.w.counters = counters_of(ws);
   const cuuint32_t es[4] = {1, 1, 1, 1};
   CUtensorMap km, vm;
   for (int which = 0; which < 2; ++which) {
@@ -571,7 +572,7 @@ bool paged_attention_few_supported(const PagedDev& kv, medusa_dtype_t dtype, int
 }
 
 size_t paged_attention_few_workspace_bytes(const PagedDev& kv, int N, int H) {
-  return counter_bytes(N, H, kv.Hkv, kv.B, 16) + 2ull * sm_count() * slot_floats(16, kv.hd) * sizeof(float);
+  return slots_bytes() + counter_bytes(N, H, kv.Hkv, kv.B, 16);
 }
 
 medusa_status_t launch_paged_attention_few(const PagedDev& kv, int N, int H, const void* q, float scale, const TreeDev* tree,

@@ -70,6 +70,7 @@ template <int HD>
 constexpr int smem_bytes() { return Shape<HD>::kOffBars + static_cast<int>(sizeof(Bars)); }
 static_assert(smem_bytes<128>() <= 232448, "shared memory budget");
 static_assert(smem_bytes<64>() <= 232448, "shared memory budget");
+static_assert(2 * slot_floats(2 * kGroup, 128) <= kSlotFloatsPerSm, "two slots per CTA");
 
 struct Params {
   Work w;
@@ -781,8 +782,8 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.box = page < kBK ? page : kBK;
   p.scale_log2 = scale * kLog2e;
   p.out = static_cast<uint16_t*>(out);
-  p.w.counters = static_cast<unsigned*>(ws);
-  p.w.slots = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + counter_bytes(N, H, kv.Hkv, kv.B, p.w.R));
+  p.w.slots = static_cast<float*>(ws);
+  p.w.counters = counters_of(ws);
   const cuuint32_t es[4] = {1, 1, 1, 1};
   CUtensorMap qm, km, vm;
   {
@@ -818,7 +819,7 @@ bool paged_attention_tc_supported(const PagedDev& kv, medusa_dtype_t dtype, int 
 
 size_t paged_attention_tc_workspace_bytes(const PagedDev& kv, int N, int H) {
   const int g = H / kv.Hkv;
-  return counter_bytes(N, H, kv.Hkv, kv.B, 2 * (kGroup / g) * g) + 2ull * sm_count() * slot_floats(2 * kGroup, kv.hd) * sizeof(float);
+  return slots_bytes() + counter_bytes(N, H, kv.Hkv, kv.B, 2 * (kGroup / g) * g);
 }
 
 medusa_status_t launch_paged_attention_tc(const PagedDev& kv, int N, int H, const void* q, float scale, const TreeDev* tree,

@@ -36,8 +36,8 @@ struct Work {
   int N, H, g;             // g = H / Hkv
   int R;                   // query rows per tile
   const int32_t* starts;
+  float* slots;            // 2 per CTA, at the start of the workspace
   unsigned* counters;      // kCounters per unit, zero between calls
-  float* slots;            // 2 per CTA
   int* status;
 };
 
@@ -149,23 +149,24 @@ struct Cut {
       p.first[b] = first[i];
       tiles[i] = tiles_of(w, n[i]);
       work[i] = n[i] > 0 ? before_tile(w, L[i], n[i], tiles[i], tiles[i]) * hk : 0ull;
+      if (work[i] > 1ull << 31) work[i] = 1ull << 31;      // too many on its own: refused below
     }
-    // Tiles (below 2^23) and blocks, summed over the lanes before in one word.
-    unsigned long long both = (work[0] + work[1]) << 23 | static_cast<unsigned>(tiles[0] + tiles[1]);
+    // Tiles (N g / R + B: below 2^25) and blocks (at most 2^37), summed over the lanes before in one word.
+    unsigned long long both = (work[0] + work[1]) << 26 | static_cast<unsigned>(tiles[0] + tiles[1]);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const unsigned long long v = __shfl_up_sync(0xffffffffu, both, o);
       if (lane >= o) both += v;
     }
-    const unsigned long long ws = both >> 23;
+    const unsigned long long ws = both >> 26;
     both = __shfl_sync(0xffffffffu, both, 31);
-    unsigned long long W = both >> 23;
+    unsigned long long W = both >> 26;
     if (W > 0x7fffffffull) {     // 2^31 blocks of keys in one call: refused like any other impossible chunk
       W = 0;
       bad = true;
     }
     if (bad && blockIdx.x == 0) set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
-    const unsigned c = blockIdx.x, C = gridDim.x, units = static_cast<unsigned>(both & 0x7fffffu) * hk;
+    const unsigned c = blockIdx.x, C = gridDim.x, units = static_cast<unsigned>(both & 0x3ffffffu) * hk;
     if (W > 0 && units < C && __all_sync(0xffffffffu, tiles[0] <= 1 && tiles[1] <= 1)) {
       // sum_u ceil(blocks_u / each) <= W / each + units <= C
       const unsigned total = static_cast<unsigned>(W), each = (total + C - units - 1) / (C - units);
@@ -308,13 +309,20 @@ struct Cut {
   }
 };
 
-// Bytes of the counters (for the largest possible number of units) and floats
-// of a slot (R rows of hd outputs, a maximum and a sum).
+// Floats of a slot (R rows of hd outputs, a maximum and a sum) and bytes of the
+// counters (for the largest possible number of units).  The slots come first
+// and take the same room whatever the call, so that calls of any shapes can
+// use one workspace in turn: none leaves its slots where another counts.
+constexpr size_t slot_floats(int R, int hd) { return static_cast<size_t>(R) * (hd + 2); }
+constexpr size_t kSlotFloatsPerSm = 2 * slot_floats(256, 128);   // the largest: each kernel asserts that its own fit
+inline size_t slots_bytes() { return align_up(sm_count() * kSlotFloatsPerSm * sizeof(float), 256); }
+inline unsigned* counters_of(void* ws) {
+  return reinterpret_cast<unsigned*>(static_cast<unsigned char*>(ws) + slots_bytes());
+}
 inline size_t counter_bytes(int N, int H, int Hkv, int B, int R) {
   const long long tiles = static_cast<long long>(N) * (H / Hkv) / R + B + 1;
   return align_up(static_cast<size_t>(tiles) * Hkv * kCounters * sizeof(unsigned), 256);
 }
-constexpr size_t slot_floats(int R, int hd) { return static_cast<size_t>(R) * (hd + 2); }
 
 }  // namespace paged
 }  // namespace medusa

@@ -58,7 +58,7 @@ __device__ Place place_token(const RopeArgs& a, int n, const int32_t* starts /* 
     b = lo;
     first = starts[b];
     last = starts[b + 1];
-    if (n < first || n >= last || last > a.N) return pl;   // behind the last sequence
+    if (first < 0 || n < first || n >= last || last > a.N) return pl;   // behind the last sequence, or no chunk
   }
   const int L = a.kv.lens[b];
   const long long cap = static_cast<long long>(a.kv.max_pages) << a.kv.page_shift;

@@ -300,6 +300,81 @@ def test_paged_attention_shared_prefix(mb):
     assert (np.abs(f64(out) - want) <= tol).all()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_paged_attention_one_workspace_in_turn(mb, dtype):
+    """Calls of all kinds share one workspace: none leaves in it what another takes for a count."""
+    big = 0
+    calls = [(128, 64, 8, 2, [300], [700]), (128, 64, 4, 4, [500, 90], [1, 1]), (128, 16, 4, 2, [40, 200, 0], [60, 7, 300]),
+             (64, 16, 4, 4, [900], [2]), (64, 8, 4, 1, [100] * 9, [9, 0, 30, 1, 1, 64, 2, 0, 5]), (256, 32, 2, 1, [600], [40])]
+    for hd, page, H, Hkv, lens, news in calls:
+        c = Cache(mb, dtype, hd, page, Hkv, lens, news)
+        big = max(big, mb.medusa_paged_attention_workspace_size(c.kv, sum(news), H))
+    ws = mb.workspace(big)
+    for turn in range(2):
+        for hd, page, H, Hkv, lens, news in calls[::1 - 2 * turn]:
+            check_attention(mb, dtype, hd, page, H, Hkv, lens, news, ws=ws)
+            check_attention(mb, dtype, hd, page, H, Hkv, lens, news, ws=ws, scale=-0.05)     # the CUDA-core kernel for bf16 too
+
+
+@pytest.mark.parametrize("dtype,hd,H,Hkv", [("bf16", 128, 4, 2), ("bf16", 64, 3, 3), ("bf16", 40, 4, 2), ("f32", 64, 2, 1)])
+def test_paged_attention_64_sequences(mb, dtype, hd, H, Hkv):
+    """The most sequences of a call, some with nothing to do and some with no prefix; then a single token each."""
+    rng = np.random.default_rng(hd)
+    lens = [int(x) for x in rng.integers(0, 70, 64)]
+    news = [int(x) for x in rng.integers(0, 9, 64)]
+    lens[0] = lens[63] = 0
+    news[5], news[0], news[63] = 150, 0, 0
+    check_attention(mb, dtype, hd, 8, H, Hkv, lens, news)
+    lens[7] = 1700
+    check_attention(mb, dtype, hd, 16, H, Hkv, lens, [1] * 64)
+
+
+def test_paged_attention_wide_groups(mb):
+    """Groups of more than 128 query heads, that 128 is no multiple of, and of the most heads."""
+    check_attention(mb, "bf16", 128, 16, 256, 1, [33], [3])
+    check_attention(mb, "bf16", 128, 16, 128, 1, [130], [3])
+    check_attention(mb, "bf16", 64, 16, 100, 1, [200, 3], [5, 2])
+    check_attention(mb, "bf16", 128, 16, 75, 1, [200], [1])
+    check_attention(mb, "bf16", 64, 8, 256, 256, [9], [1])
+
+
+def test_offsets_past_32_bits(mb):
+    """Pages whose elements lie past 2^31 (and bytes past 2^32), in the second layer: append, attention, compaction."""
+    hd, page, Hkv, H, n_pages = 128, 256, 40, 40, 1700                # 1700 * 40 * 256 * 128 > 2^31 elements a layer
+    k = torch.empty(2, n_pages, Hkv, page, hd, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    tree = mb.Tree(O.ranksum_choices(3, 2, 14), 3, 2)
+    T, L = tree.T, 250                                                # the new rows begin in one page and end in the next
+    used = [n_pages - 1, n_pages - 2]
+    g = torch.Generator(device="cuda").manual_seed(5)
+    k[1, used] = torch.randn(2, Hkv, page, hd, generator=g, device="cuda").bfloat16()
+    v[1, used] = torch.randn(2, Hkv, page, hd, generator=g, device="cuda").bfloat16()
+    k[0, used], v[0, used] = 0, 0
+    lens = ints([L])
+    kv = mb.PagedKV(k, v, ints([used]), lens)
+    q = torch.randn(T, H, hd, generator=g, device="cuda").bfloat16()
+    nk, nv = (torch.randn(T, Hkv, hd, generator=g, device="cuda").bfloat16() for _ in range(2))
+    small = mb.PagedKV(k[:, used].contiguous(), v[:, used].contiguous(), ints([[0, 1]]), ints([L]))
+    assert k[1, used[0]].data_ptr() - k.data_ptr() > 2 ** 33
+    outs = []
+    for cache in (kv, small):                                         # the same pages near the buffer's start: the same bits
+        qr, out = torch.empty_like(q), torch.empty_like(q)
+        mb.medusa_rope_append(cache, 1, q, nk, nv, qr, mb.Rotary(hd))
+        ws = mb.workspace(mb.medusa_paged_attention_workspace_size(cache, T, H))
+        mb.medusa_paged_attention(cache, 1, qr, out, hd ** -0.5, ws, tree=tree)
+        best = max(range(tree.P), key=lambda p: sum(x >= 0 for x in tree.tables()["retrieve"][p]))
+        mb.medusa_paged_accept_kv(tree, cache, ints([best]), ints([tree.D]), cache.seq_lens,
+                                  mb.workspace(mb.medusa_paged_accept_workspace_size(cache)))
+        outs.append((out, cache.seq_lens.clone()))
+    assert torch.equal(outs[0][0], outs[1][0]) and outs[0][0].isfinite().all() and outs[0][1].tolist() == [L + tree.D + 1]
+    for far, near in ((k, small.k_pages), (v, small.v_pages)):
+        assert torch.equal(far[:, used], near)
+    rows = [(0, r) if r < page else (1, r - page) for r in range(L, L + T)]
+    moved = small.v_pages[1][[p for p, _ in rows], :, [r for _, r in rows]]
+    path = tree.tables()["retrieve"][best]
+    assert torch.equal(moved[:tree.D + 1], nv[[int(x) for x in path[:tree.D + 1]]])
+
+
 # ---------------------------------------------------------------------------
 # compaction
 # ---------------------------------------------------------------------------
@@ -419,6 +494,39 @@ def test_adjust_logits(mb, case, in_place):
     assert few.all()
 
 
+def test_adjust_logits_past_32_bits(mb):
+    """Rows that begin past 2^31 elements, in place: the last sequence's equal those of a call of its own."""
+    tree = mb.Tree(O.ranksum_choices(5, 10, 63), 5, 10)
+    B, T, V = 35, 64, 960_001
+    assert B * T * V > 2 ** 31
+    z = torch.empty(B, T, V, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    last = torch.randn(1, T, V, generator=g, device="cuda")
+    z[:-1], z[-1:] = 0, last
+    tokens = ints([[(7 * i) % V for i in range(T)]] * B)
+    kw = dict(presence=torch.full((B,), 0.5, device="cuda"), repetition=torch.full((B,), 1.25, device="cuda"),
+              bias_ids=ints([[V - 1, 5]] * B), bias=torch.ones(B, 2, device="cuda"))
+    mb.medusa_adjust_logits(tree, z, tokens, z, **kw)
+    want = torch.empty_like(last)
+    mb.medusa_adjust_logits(tree, last, tokens[-1:].contiguous(), want, **{k: x[-1:].contiguous() for k, x in kw.items()})
+    assert torch.equal(z[-1:], want) and not torch.equal(want, last)
+    assert (z[0, 0, V - 1], z[0, 0, 5], z[0, 0, 0], z[0, 0, 1]) == (1.0, 1.0, -0.5, 0.0)
+
+
+def test_adjust_logits_infinite(mb):
+    """Infinite and NaN logits and biases follow the definition's arithmetic."""
+    tree = mb.Tree([], 1, 1)
+    inf, nan = float("inf"), float("nan")
+    z = torch.tensor([[[inf, -inf, nan, 1.0, -2.0, 3.0, -inf, 0.0]]], device="cuda")
+    out = torch.empty_like(z)
+    ok = ints([[[0b01111111]]])
+    mb.medusa_adjust_logits(tree, z, ints([[1]]), out, repetition=torch.tensor([2.0], device="cuda"),
+                            presence=torch.tensor([0.25], device="cuda"), history=ints([[0, 2, 3, 4]]), history_lens=ints([4]),
+                            bias_ids=ints([[5, 6]]), bias=torch.tensor([[-inf, 9.0]], device="cuda"), allowed=ok)
+    got = out.flatten().tolist()
+    assert got[:2] == [inf, -inf] and np.isnan(got[2]) and got[3:] == [0.25, -4.25, -inf, -inf, -inf]
+
+
 def test_adjust_logits_odd_alignment(mb):
     """Logits that start 4 bytes past a 16-byte boundary take the element path."""
     tree = mb.Tree(O.ranksum_choices(2, 2, 6), 2, 2)
@@ -482,6 +590,22 @@ def test_device_checks_of_chunks(mb):
             assert (out[4:] == 7).all()
 
 
+def test_device_checks_of_rope_chunks(mb):
+    """A chunk that begins before row 0 or ends behind the last is not written; the others are."""
+    c = Cache(mb, "bf16", 128, 16, 2, [20, 10, 0], [2, 2, 2])
+    q, k = c.randn(6, 2, 128).bfloat16().cuda(), c.randn(6, 2, 128).bfloat16().cuda()
+    rotary = mb.Rotary(128)
+    good = torch.empty_like(q)
+    mb.medusa_rope_append(c.kv, 0, q, k, k, good, rotary)
+    for starts, ok in (([0, 2, 4, 9], [0, 1, 2, 3]), ([-3, 2, 4, 6], [2, 3, 4, 5])):
+        out, before = torch.full_like(q, 7.0), c.k.clone()
+        mb.medusa_rope_append(c.kv, 0, q, k, k, out, rotary, chunk_starts=ints(starts))
+        assert mb.device_status() == (mb.MEDUSA_ERR_DEVICE_CHECK, 11)
+        for n in range(6):
+            assert torch.equal(out[n], good[n]) if n in ok else (out[n] == 7).all()
+        assert torch.equal(c.k.view(torch.uint8), before.view(torch.uint8))      # the same rows, written again
+
+
 def test_device_checks_of_accept_and_logits(mb):
     tree = mb.Tree(O.ranksum_choices(2, 2, 6), 2, 2)
     c = Cache(mb, "bf16", 64, 16, 2, [20, 10], [7, 7])
@@ -528,6 +652,27 @@ def test_other_stream_and_graph(mb):
     mb.medusa_paged_attention(c.kv, 0, q, want, 128 ** -0.5, ws2)
     # sequence 1's own row (41) was never written: NaN in both
     assert np.array_equal(f64(got), f64(want), equal_nan=True) and got[[0, 2]].isfinite().all()
+
+
+def test_two_graphs_at_once(mb):
+    """Two captured calls with workspaces of their own, replayed at the same time on two streams, many times."""
+    jobs = []
+    for seed, (lens, news) in enumerate((([300, 1200], [70, 5]), ([2000, 40, 129], [1, 1, 1]))):
+        c, q, want = check_attention(mb, "bf16", 128, 16, 8, 2, lens, news, seed=seed)
+        ws = mb.workspace(mb.medusa_paged_attention_workspace_size(c.kv, sum(news), 8))
+        got, starts = torch.zeros_like(want), ints(starts_of(news))
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph):
+            mb.medusa_paged_attention(c.kv, 0, q, got, 128 ** -0.5, ws, chunk_starts=starts)
+        jobs.append((graph, stream, got, want, c, q, ws, starts))
+    torch.cuda.synchronize()
+    for _ in range(50):
+        for graph, stream, *_ in jobs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, _, got, want, *_ in jobs:
+        assert torch.equal(got, want)
 
 
 def test_a_verification_step_over_pages(mb):

@@ -340,7 +340,8 @@ def test_c_well_formed_calls_reach_the_device_check(mb, tree):
 
 
 @no_gpu
-@pytest.mark.parametrize("over", [dict(H=3), dict(q=None), dict(ws=None), dict(out=5 * P), dict(scale=math.inf), dict(ws=7 * P + 16),
+@pytest.mark.parametrize("over", [dict(H=3), dict(q=None), dict(ws=None), dict(out=5 * P), dict(scale=math.inf), dict(scale=-math.inf),
+                                  dict(scale=math.nan), dict(scale=2.0 ** 65), dict(ws=7 * P + 16),
                                   dict(layer=9), dict(N=5)], ids=str)
 def test_c_paged_attention(mb, over):
     a = dict(layer=0, N=6, H=4, q=5 * P, scale=0.1, out=6 * P, ws=7 * P)
@@ -362,7 +363,7 @@ def test_c_accept_and_logits(mb, tree):
     r = mb.LogitRules()
     adj = lambda rules, B=2, V=50, z=5 * P, tok=6 * P, out=7 * P: mb._lib.medusa_adjust_logits(  # noqa: E731
         tree.handle, B, V, z, tok, ctypes.byref(rules), out, None)
-    for kw in (dict(B=0), dict(B=65), dict(V=0), dict(z=None), dict(out=None)):
+    for kw in (dict(B=0), dict(B=65), dict(V=0), dict(V=2 ** 30 + 1), dict(z=None), dict(out=None)):
         assert adj(r, **kw) == 1
     assert adj(r) == 1 and b"without upload" in mb._lib.medusa_last_error()
     for fields, kw in ((dict(history=P), {}), (dict(history=P, history_lens=P), {}), (dict(prompt_lens=P), {}),
