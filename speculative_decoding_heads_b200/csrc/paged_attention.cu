@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       const int r = i / (HD / 4), d = i - r * (HD / 4);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
       if (r < rows && d < hd4) {
-        const int rr = x.tile * R + r, tok = rr / g, head = x.h * g + rr - tok * g;
+        const int rr = x.tile * R + r, tok = rr / w.by_g, head = x.h * g + rr - tok * g;
         v = load4<T>(q + (static_cast<size_t>(first + tok) * w.H + head) * hd + 4 * d);
       }
       *reinterpret_cast<float4*>(qs + r * S::kPitch + 4 * d) = v;
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       __syncthreads();                     // P goes where K was
 #pragma unroll
       for (int r = 0; r < RR; ++r) {
-        const int rr = x.tile * R + ty * RR + r, tok = rr / g;
+        const int rr = x.tile * R + ty * RR + r, tok = rr / w.by_g;
         float mx = -INFINITY;
         // Nodes j0 - L .. of the tree that this row sees, one bit per key of the block.
         uint64_t sees = 0ull;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       for (int r = 0; r < RR; ++r) {
         const int row = ty * RR + r;
         if (row >= rows) continue;
-        const int rr = x.tile * R + row, tok = rr / g, head = x.h * g + rr - tok * g;
+        const int rr = x.tile * R + row, tok = rr / w.by_g, head = x.h * g + rr - tok * g;
         const float inv = 1.f / l[r];
         T* dst = out + (static_cast<size_t>(first + tok) * w.H + head) * hd;
 #pragma unroll
@@ -360,6 +360,8 @@ medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype,
   w.status = device_status_ptr();
   const Choice c = choose(kv, N, H);
   w.R = c.R;
+  w.by_g = Divisor(w.g);
+  w.by_R = Divisor(w.R);
   w.slots = static_cast<float*>(ws);
   w.counters = counters_of(ws);
   const int grid = sm_count() * c.per_sm;

@@ -165,8 +165,9 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
       ph ^= 1;
     }
   };
-  auto all = [&] {                                     // the 256 computing threads
-    mbar_arrive_cta(&bar->group);
+  auto all = [&] {                                     // the computing warps
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cta(&bar->group);
     return wait(&bar->group, syncs++ & 1, bar, status);
   };
   // ldmatrix rows: K (keys x dimensions) and V (transposed) of this warp's 16 keys.
@@ -180,14 +181,14 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
     const int row0 = x.tile * S::kRows, rows = min(S::kRows, n * g - row0);
     const int keys = C::keys(p.w, pl, b, x.tile);
     const bool tree = p.w.t.T > 0;
-    const int clear = tree ? L : L + row0 / g + 1;     // below every row's limit
+    const int clear = tree ? L : L + row0 / p.w.by_g + 1;     // below every row's limit
     int tok[2];                                    // tokens of this thread's rows
     uint32_t sees[2];                              // and the tree's nodes that they see (T <= 16 here)
     uint32_t qa[HD / 16][4];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = 8 * i + gr, rr = row0 + r;
-      tok[i] = rr / g;
+      tok[i] = rr / p.w.by_g;
       sees[i] = tree && r < rows ? static_cast<uint32_t>(p.w.t.anc[tok[i]]) : 0u;
       const uint16_t* src = p.q + (static_cast<size_t>(first + tok[i]) * p.w.H + x.h * g + rr - tok[i] * g) * HD + 2 * qc;
 #pragma unroll
@@ -365,7 +366,7 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
     const bool whole = C::whole(x);
     float* slot = p.w.slots + C::slot(pl, blockIdx.x, x.start) * slot_floats(S::kRows, HD);
     auto place = [&](int r) {
-      const int t = (row0 + r) / g;
+      const int t = (row0 + r) / p.w.by_g;
       return p.out + (static_cast<size_t>(first + t) * p.w.H + x.h * g + row0 + r - t * g) * HD;
     };
     for (int i = tid; i < rows * kC4; i += 32 * kWarps) {
@@ -488,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bar->full[st], 1);
         mbar_init(&bar->empty[st], kWarps);
       }
-      mbar_init(&bar->group, 32 * kWarps);
+      mbar_init(&bar->group, kWarps);
       bar->abort = 0;
       fence_barrier_init();
     }
@@ -529,6 +530,8 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.H = H;
   p.w.g = H / kv.Hkv;
   p.w.R = S::kRows;
+  p.w.by_g = Divisor(p.w.g);
+  p.w.by_R = Divisor(p.w.R);
   p.w.starts = starts;
   p.w.status = device_status_ptr();
   const int page = 1 << kv.page_shift;

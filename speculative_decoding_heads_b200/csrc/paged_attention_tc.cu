@@ -11,7 +11,8 @@
 // by the tensor cores and the exponentials).  A unit of fewer rows gives the
 // key tiles to the warpgroups alternately, each with its own O, m and l
 // (tokens and trees: bound by the cache's bytes); the two are joined with
-// factors 2^(m_w - m) when they are written.
+// factors 2^(m_w - m) when they are written, by the first warpgroup while the
+// second takes the next unit's first tile.
 //
 // The maximum is moved (and O rescaled) only when a tile's exceeds it by more
 // than 2^8: any reference that keeps the exponents finite gives the same
@@ -59,7 +60,7 @@ struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2];
-  uint64_t stat_full, stat_free, group[2];   // statistics handed over; the threads of one warpgroup
+  uint64_t stat_full, stat_free, group[2];   // statistics handed over; the warps of one warpgroup
   uint32_t tmem_base;
   int abort, last[2];
   float m1[kGroup], l1[kGroup];          // alternating units: the second warpgroup's statistics
@@ -180,7 +181,7 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
     if (lane == 0) {
       mbar_arrive_expect_tx(&bar->q_full[w], S::kHalves * p.w.g * p.q_tokens * 128);
       for (int hf = 0; hf < S::kHalves; ++hf)
-        tc::tma_load_4d(smem + w * S::kTile + hf * S::kHalf, q_map, 0, h * p.w.g, pl.first[b] + row0 / p.w.g, hf, &bar->q_full[w]);
+        tc::tma_load_4d(smem + w * S::kTile + hf * S::kHalf, q_map, 0, h * p.w.g, pl.first[b] + row0 / p.w.by_g, hf, &bar->q_full[w]);
     }
     ++nq[w];
     return true;
@@ -320,15 +321,17 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
     } else {
       for (int i = 0; i < 2 && i < s.n; ++i) {
         if (!landed()) return;
-        scores(i, 0, true, i + 1 == s.n);
+        scores(1 - i, 0, true, i + 1 == s.n);
         next();
       }
+      // No phase of a barrier goes by unseen, where the first warpgroup has no tile either.
+      if (s.n == 1 && piece > 0 && !wait(&bar->o_free[0], (piece - 1) & 1, bar, status)) return;
       for (int i = 0; i < s.n; ++i) {
-        if (!values(i & 1, i < 2, tile_chunks(keys - (x.kb0 + i) * kBK), true)) return;
+        if (!values(1 - (i & 1), i < 2, tile_chunks(keys - (x.kb0 + i) * kBK), true)) return;
         next();
         if (i + 2 < s.n) {
           if (!landed()) return;
-          scores(i & 1, 0, true, i + 3 == s.n);
+          scores(1 - (i & 1), 0, true, i + 3 == s.n);
           next();
         }
       }
@@ -464,28 +467,43 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
     const int grp_row = x.tile * p.w.R + (s.two ? w * p.rows : 0);   // this group's first row
     const int rows = s.two ? (w == 0 ? p.rows : s.rows - p.rows) : s.rows;
     const bool active = 32 * quarter < rows; // a warp without rows only keeps the barriers going
-    const int tok = (grp_row + row) / p.w.g;
+    const int tok = (grp_row + row) / p.w.by_g;
     const int keys = C::keys(p.w, pl, b, x.tile);
     const bool tree = p.w.t.T > 0;
-    uint64_t anc[4] = {0ull, 0ull, 0ull, 0ull};
-    if (tree && row < rows) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (i < p.w.t.W) anc[i] = p.w.t.anc[tok * p.w.t.W + i];
-    }
     // Keys below this row's limit are visible (chunks); a tile below every row's limit needs no mask.
     const int limit = L + min(tok, n - 1) + 1;
-    const int clear = tree ? L : L + grp_row / p.w.g + 1;
+    const int clear = tree ? L : L + grp_row / p.w.by_g + 1;
     float m = -INFINITY, l = 0.f;
-    auto hand_over = [&](uint64_t* to) {
-      tc::fence_before_sync();
+    // One arrival per warp: those of 128 threads on one barrier took 1000 clocks.
+    auto arrive = [&](uint64_t* to) {
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(to);
     };
-    for (int i = s.two ? 0 : w; i < s.n; i += s.two ? 1 : 2, ++steps) {
+    auto hand_over = [&](uint64_t* to) {
+      tc::fence_before_sync();
+      arrive(to);
+    };
+    for (int i = s.two ? 0 : 1 - w; i < s.n; i += s.two ? 1 : 2, ++steps) {
+      const int j0 = (x.kb0 + i) * kBK;
+      // The keys that this row sees, looked up while S is on its way.
+      uint32_t bits[4] = {0u, 0u, 0u, 0u};
+      if (j0 + kBK > clear) {
+        if (!tree) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int lim = limit - j0 - 32 * c;
+            bits[c] = lim >= 32 ? ~0u : lim <= 0 ? 0u : (1u << lim) - 1u;
+          }
+        } else if (row < rows) {
+          uint64_t anc[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) anc[k] = k < p.w.t.W ? p.w.t.anc[tok * p.w.t.W + k] : 0ull;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) bits[c] = static_cast<uint32_t>(tree_bits(anc, L - j0 - 32 * c));
+        }
+      }
       if (!wait(&bar->s_full[w], steps & 1, bar, status)) return;
       tc::fence_after_sync();
-      const int j0 = (x.kb0 + i) * kBK;
       const bool zero = (w == 0 || !s.two) && x.kb0 + i == x.blocks - 1 && (keys & (p.box - 1)) != 0;
       if (active) {
         float sv[kBK];
@@ -493,16 +511,6 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         for (int c = 0; c < kBK; c += 32) tc::tmem_ld32(tS + c, sv + c);
         tc::tmem_wait_ld();
         if (j0 + kBK > clear) {
-          uint32_t bits[4];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (tree) {
-              bits[c] = static_cast<uint32_t>(tree_bits(anc, L - j0 - 32 * c));
-            } else {
-              const int lim = limit - j0 - 32 * c;
-              bits[c] = lim >= 32 ? ~0u : lim <= 0 ? 0u : (1u << lim) - 1u;
-            }
-          }
 #pragma unroll
           for (int k = 0; k < kBK; ++k) sv[k] = (bits[k >> 5] >> (k & 31)) & 1u ? sv[k] : -INFINITY;
         }
@@ -573,9 +581,9 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
 
     // Output, a row per thread.  Where the tiles alternated, the second
     // warpgroup hands over its statistics and the first joins and writes both.
-    const int n0 = s.two ? s.n : (s.n + 1) / 2, n1 = s.two ? s.n : s.n / 2;
+    const int n0 = s.two ? s.n : s.n / 2, n1 = s.two ? s.n : (s.n + 1) / 2;
     entries += 2 * s.n;
-    bool second = false;                       // O_1 belongs to this thread's row as well
+    bool second = false;                       // both O_0 and O_1 belong to this thread's row
     float f0 = 1.f, f1 = 0.f;
     if (!s.two) {
       if (w == 1) {
@@ -583,22 +591,23 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         if (singles > 0 && !wait(&bar->stat_free, (singles - 1) & 1, bar, status)) return;
         bar->m1[row] = m;
         bar->l1[row] = l;
-        tc::mbar_arrive(&bar->stat_full);
+        arrive(&bar->stat_full);
       } else {
         if (!wait(&bar->stat_full, singles & 1, bar, status)) return;
         const float m1 = bar->m1[row], l1 = bar->l1[row], mm = fmaxf(m, m1);
-        tc::mbar_arrive(&bar->stat_free);
+        arrive(&bar->stat_free);
         f0 = m == -INFINITY ? 0.f : tc::ex2_ftz(m - mm);
         f1 = m1 == -INFINITY ? 0.f : tc::ex2_ftz(m1 - mm);
         m = mm;
         l = f0 * l + f1 * l1;
-        second = n1 > 0;
+        second = n0 > 0;
       }
       ++singles;
     }
     if (s.two || w == 0) {
-      if (!wait(&bar->pv_done[w], (pv[w] + (w == 0 ? n0 : n1) - 1) & 1, bar, status)) return;
-      if (second && !wait(&bar->pv_done[1], (pv[1] + n1 - 1) & 1, bar, status)) return;
+      const int own = s.two ? w : 1;           // the first tile of an alternating unit is the second warpgroup's
+      if (second && !wait(&bar->pv_done[0], (pv[0] + n0 - 1) & 1, bar, status)) return;
+      if (!wait(&bar->pv_done[own], (pv[own] + (own == 0 ? n0 : n1) - 1) & 1, bar, status)) return;
       tc::fence_after_sync();
       const bool whole = C::whole(x);
       const int slot_row = (s.two ? w * kGroup : 0) + row;           // rows of a slot: 2 * kGroup
@@ -607,21 +616,22 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
       const float inv = 1.f / l;
       // Columns c .. c + 3 of row r of the group.
       auto put = [&](int r, int c, uint2 v) {
-        const int t = (grp_row + r) / p.w.g;
+        const int t = (grp_row + r) / p.w.by_g;
         *reinterpret_cast<uint2*>(p.out + (static_cast<size_t>(pl.first[b] + t) * p.w.H + x.h * p.w.g + (grp_row + r - t * p.w.g)) * HD + c) = v;
       };
       if (active) {
 #pragma unroll 1
         for (int c = 0; c < HD; c += 32) {
           float o[32];
-          tc::tmem_ld32(tmem + lanes + 256 + 128 * w + c, o);
-          tc::tmem_wait_ld();
+          tc::tmem_ld32(tmem + lanes + 256 + 128 * own + c, o);
           if (second) {
-            float o1[32];
-            tc::tmem_ld32(tmem + lanes + 384 + c, o1);
+            float o0[32];
+            tc::tmem_ld32(tmem + lanes + 256 + c, o0);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = fmaf(o1[k], f1, o[k] * f0);
+            for (int k = 0; k < 32; ++k) o[k] = fmaf(o0[k], f0, o[k] * f1);
+          } else {
+            tc::tmem_wait_ld();
           }
           if (whole) {
             if (row < rows)
@@ -649,7 +659,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           __stcg(slot + 2 * kGroup + slot_row, l);
         }
         __threadfence();
-        tc::mbar_arrive(&bar->group[w]);
+        arrive(&bar->group[w]);
         if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
         int lo, hi;
         C::owners(pl, x, lo, hi);
@@ -658,7 +668,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           bar->last[w] = atom_add_acq_rel_gpu(ctr, 1u) == static_cast<unsigned>(hi - lo);
           if (bar->last[w]) *ctr = 0u;
         }
-        tc::mbar_arrive(&bar->group[w]);
+        arrive(&bar->group[w]);
         if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
         if (bar->last[w]) {
           __threadfence();
@@ -705,10 +715,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bar->p_full[w], 4);
         mbar_init(&bar->pv_done[w], 1);
         mbar_init(&bar->o_free[w], 4);
-        mbar_init(&bar->group[w], kGroup);
+        mbar_init(&bar->group[w], 4);
       }
-      mbar_init(&bar->stat_full, kGroup);
-      mbar_init(&bar->stat_free, kGroup);
+      mbar_init(&bar->stat_full, 4);
+      mbar_init(&bar->stat_free, 4);
       bar->abort = 0;
       fence_barrier_init();
     }
@@ -776,6 +786,8 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   const int tokens = kGroup / p.w.g;
   p.rows = tokens * p.w.g;
   p.w.R = 2 * p.rows;
+  p.w.by_g = Divisor(p.w.g);
+  p.w.by_R = Divisor(p.w.R);
   const int most = starts ? N : N / kv.B;                // tokens of one sequence
   p.q_tokens = tokens < most ? tokens : most;
   const int page = 1 << kv.page_shift;

@@ -30,11 +30,29 @@ namespace paged {
 
 constexpr int kCounters = 2;   // per unit: row groups that are joined on their own
 
+// x / d for 0 <= x < 2^31 and 1 <= d <= 2^15 as one product: with 2^k >= d and
+// m = ceil(2^(31+k) / d), x m / 2^(31+k) exceeds x / d by less than 2^-k <= 1/d.
+// (The chain of divisions between two units took the products' warp 2000 clocks.)
+struct Divisor {
+  unsigned m;
+  int shift;
+  Divisor() = default;
+  explicit Divisor(unsigned d) {
+    shift = 31;
+    while ((1u << (shift - 31)) < d) ++shift;
+    m = static_cast<unsigned>(((1ull << shift) + d - 1) / d);
+  }
+};
+__device__ __forceinline__ int operator/(int x, const Divisor& d) {
+  return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(x)) * d.m) >> d.shift);
+}
+
 struct Work {
   PagedDev kv;
   TreeDev t;               // T = 0: causal chunks
   int N, H, g;             // g = H / Hkv
   int R;                   // query rows per tile
+  Divisor by_g, by_R;
   const int32_t* starts;
   float* slots;            // 2 per CTA, at the start of the workspace
   unsigned* counters;      // kCounters per unit, zero between calls
@@ -43,8 +61,8 @@ struct Work {
 
 struct Plan {
   int L[MEDUSA_MAX_B], n[MEDUSA_MAX_B], first[MEDUSA_MAX_B];
-  unsigned total;                      // W: key blocks of all units
   unsigned each;                       // cut at unit boundaries: blocks per CTA; 0: equal ranges
+  unsigned per, more;                  // equal ranges: blocks of a CTA, and how many of the first hold one more
   unsigned begin, end;                 // this CTA's range
   int b, h, tile, block;               // where it starts
   int lo, hi;                          // cut at unit boundaries: the CTAs of its unit
@@ -86,7 +104,7 @@ struct Cut {
   static __device__ __forceinline__ int keys(const Work& w, const Plan& p, int b, int tile) {
     const int n = p.n[b];
     if (w.t.T > 0) return p.L[b] + n;
-    const int last = ((tile + 1) * w.R - 1) / w.g + 1;
+    const int last = ((tile + 1) * w.R - 1) / w.by_g + 1;
     return p.L[b] + (last < n ? last : n);
   }
   static __device__ __forceinline__ int blocks(const Work& w, const Plan& p, int b, int tile) {
@@ -104,7 +122,7 @@ struct Cut {
         k == 0 ? 0ull : static_cast<unsigned long long>(k) * q + floor_sum(k, m, w.R, w.g * r + w.R + m - 1);
     return t < tiles ? s : s + all;
   }
-  static __device__ __forceinline__ int tiles_of(const Work& w, int n) { return (n * w.g + w.R - 1) / w.R; }
+  static __device__ __forceinline__ int tiles_of(const Work& w, int n) { return (n * w.g + w.R - 1) / w.by_R; }
 
   // One whole warp; the other threads see the plan after the next __syncthreads.
   static __device__ void plan(const Work& w, Plan& p) {
@@ -172,7 +190,6 @@ struct Cut {
       const unsigned total = static_cast<unsigned>(W), each = (total + C - units - 1) / (C - units);
       if (each <= total / C + 2) {
         if (lane == 0) {
-          p.total = total;
           p.each = each;
           p.begin = p.end = 0;
         }
@@ -206,11 +223,14 @@ struct Cut {
         return;
       }
     }
-    const unsigned r = ranges(static_cast<unsigned>(W));
-    const unsigned begin = c < r ? range_begin(c, static_cast<unsigned>(W)) : 0u;
-    const unsigned end = c < r ? range_begin(c + 1, static_cast<unsigned>(W)) : 0u;
+    // No more ranges than blocks, so that none is empty.
+    const unsigned r = W < C ? static_cast<unsigned>(W) : C, per = r > 0 ? static_cast<unsigned>(W) / r : 0u;
+    const unsigned more = static_cast<unsigned>(W) - per * r;
+    const unsigned begin = c < r ? range_begin(c, per, more) : 0u;
+    const unsigned end = c < r ? range_begin(c + 1, per, more) : 0u;
     if (lane == 0) {
-      p.total = static_cast<unsigned>(W);
+      p.per = per;
+      p.more = more;
       p.each = 0u;
       p.begin = begin;
       p.end = end;
@@ -246,20 +266,17 @@ struct Cut {
     }
   }
 
-  // No more ranges than blocks, so that none is empty; the first W mod C hold one block more.
-  static __device__ __forceinline__ unsigned ranges(unsigned W) { return W < gridDim.x ? W : gridDim.x; }
-  static __device__ __forceinline__ unsigned range_begin(unsigned c, unsigned W) {
-    const unsigned C = ranges(W), each = W / C, more = W - each * C;
-    return each * c + (c < more ? c : more);
+  static __device__ __forceinline__ unsigned range_begin(unsigned c, unsigned per, unsigned more) {
+    return per * c + (c < more ? c : more);
   }
   // The CTAs that hold a piece's unit.
   static __device__ __forceinline__ void owners(const Plan& p, const Piece& x, int& lo, int& hi) {
-    lo = p.each ? p.lo : owner(x.start, p.total);
-    hi = p.each ? p.hi : owner(x.start + x.blocks - 1, p.total);
+    lo = p.each ? p.lo : owner(p, x.start);
+    hi = p.each ? p.hi : owner(p, x.start + x.blocks - 1);
   }
-  static __device__ __forceinline__ int owner(unsigned off, unsigned W) {
-    const unsigned C = ranges(W), each = W / C, more = W - each * C;
-    return off < more * (each + 1) ? off / (each + 1) : more + (off - more * (each + 1)) / each;
+  static __device__ __forceinline__ int owner(const Plan& p, unsigned off) {
+    const unsigned longer = p.more * (p.per + 1);
+    return off < longer ? off / (p.per + 1) : p.more + (off - longer) / p.per;
   }
 
   // The first piece of a CTA's range, and the one after `x`; `left` counts the
@@ -299,13 +316,13 @@ struct Cut {
 
   // Chunks do not overlap, so floor(first g / R) + b starts a sequence's tiles clear of the one before.
   static __device__ __forceinline__ unsigned* counter(const Work& w, const Plan& p, const Piece& x) {
-    const int tile0 = p.first[x.b] * w.g / w.R + x.b;
+    const int tile0 = p.first[x.b] * w.g / w.by_R + x.b;
     return w.counters + (static_cast<size_t>(tile0 + x.tile) * w.kv.Hkv + x.h) * kCounters;
   }
   // Which of CTA c's two slots holds its piece of the unit starting at
   // `start`: the first if the unit began before the CTA's range.
   static __device__ __forceinline__ int slot(const Plan& p, int c, unsigned start) {
-    return 2 * c + (p.each || start < range_begin(c, p.total) ? 0 : 1);
+    return 2 * c + (p.each || start < range_begin(c, p.per, p.more) ? 0 : 1);
   }
 };
 
