@@ -229,8 +229,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
           __stcg(reinterpret_cast<float4*>(slot + 2 * R + row * HD + 64 * d + 4 * tx),
                  make_float4(o[r][d][0], o[r][d][1], o[r][d][2], o[r][d][3]));
       }
-      __threadfence();
-      __syncthreads();
+      __syncthreads();                     // then one thread's release covers all of them
       int c_lo, c_hi;
       C::owners(plan, x, c_lo, c_hi);
       if (tid == 0) {
@@ -241,7 +240,6 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       __syncthreads();
       write = s_last != 0;
       if (write) {
-        __threadfence();
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
           const int row = ty * RR + r;
@@ -362,6 +360,7 @@ medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype,
   w.R = c.R;
   w.by_g = Divisor(w.g);
   w.by_R = Divisor(w.R);
+  w.by_hk = Divisor(kv.Hkv);
   w.slots = static_cast<float*>(ws);
   w.counters = counters_of(ws);
   const int grid = sm_count() * c.per_sm;

@@ -122,9 +122,7 @@ __device__ void run_loads(const CUtensorMap* k_map, const CUtensorMap* v_map, co
     __syncwarp();
     if (lane < sub) {
       const int row = (kb * kBK + lane * p.box) & mask;
-#pragma unroll
-      for (int hf = 0; hf < S::kHalves; ++hf)
-        tc::tma_load_4d(d + hf * S::kHalf + lane * p.box * 128, map, 0, row, hf, block, &bar->full[st]);
+      tc::tma_load_4d(d + lane * p.box * 128 * S::kHalves, map, 0, row, 0, block, &bar->full[st]);
     }
     ++e;
     return true;
@@ -173,8 +171,12 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
   // ldmatrix rows: K (keys x dimensions) and V (transposed) of this warp's 16 keys.
   const int k_key = 16 * warp + (lane >> 4) * 8 + (lane & 7), k_ch = (lane >> 3) & 1;
   const int v_key = 16 * warp + ((lane >> 3) & 1) * 8 + (lane & 7), v_ch = lane >> 4;
-  auto at = [&](uint32_t tile, int key, int chunk) {   // 16-byte chunk of a row in the 128-byte swizzle
-    return tile + (chunk >> 3) * S::kHalf + key * 128 + (((chunk & 7) ^ (key & 7)) << 4);
+  // A tile is its boxes one after the other, each [halves][rows][64] in the 128-byte swizzle.
+  const int box = p.box;
+  auto key_at = [&](int key) { return (key & ~(box - 1)) * 128 * S::kHalves + (key & (box - 1)) * 128; };
+  const int k_at = key_at(k_key), v_at = key_at(v_key);
+  auto at = [&](uint32_t tile, int off, int key, int chunk) {   // 16-byte chunk of a row
+    return tile + (chunk >> 3) * box * 128 + off + (((chunk & 7) ^ (key & 7)) << 4);
   };
   for (;;) {
     const int b = x.b, L = pl.L[b], n = pl.n[b], first = pl.first[b];
@@ -217,7 +219,7 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
 #pragma unroll
         for (int c = 0; c < HD / 16; ++c) {
           uint32_t kf[4];
-          ldmatrix4(kf, at(kt, k_key, 2 * c + k_ch));
+          ldmatrix4(kf, at(kt, k_at, k_key, 2 * c + k_ch));
           mma(s[0], qa[c], kf[0], kf[1]);
           mma(s[1], qa[c], kf[2], kf[3]);
         }
@@ -288,17 +290,17 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
       if (mine > 0) {
         const bool stale = mine < 16;                  // rows past the sequence may hold anything: 0 * value must stay 0
         if (stale) {
-          unsigned char* d = smem + st * S::kTile + (16 * warp + mine) * 128;
           for (int i = lane; i < (16 - mine) * 8 * S::kHalves; i += 32) {
-            const int hf = i / ((16 - mine) * 8), c = i - hf * (16 - mine) * 8;
-            *reinterpret_cast<uint4*>(d + hf * S::kHalf + c * 16) = make_uint4(0, 0, 0, 0);
+            const int r = i / (8 * S::kHalves), c = i - r * 8 * S::kHalves;
+            *reinterpret_cast<uint4*>(smem + st * S::kTile + key_at(16 * warp + mine + r) + (c >> 3) * box * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
           }
           __syncwarp();
         }
 #pragma unroll
         for (int c = 0; c < kN / 2; ++c) {
           uint32_t vf[4];
-          ldmatrix4t(vf, at(vt, v_key, 2 * c + v_ch));
+          ldmatrix4t(vf, at(vt, v_at, v_key, 2 * c + v_ch));
           mma(o[2 * c], ph_, vf[0], vf[1]);
           mma(o[2 * c + 1], ph_, vf[2], vf[3]);
           mma(o[2 * c], pl_, vf[0], vf[1]);
@@ -398,8 +400,7 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
       }
     }
     if (!whole) {
-      __threadfence();
-      if (!all()) return;
+      if (!all()) return;                              // then one thread's release covers all of them
       int lo, hi;
       C::owners(pl, x, lo, hi);
       if (tid == 0) {
@@ -409,10 +410,11 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
       }
       if (!all()) return;
       if (bar->last) {
-        // The last piece joins them all in range order: `teams` of threads take
-        // every teams-th piece each, four at a time, and are joined in order.
-        __threadfence();
-        const int items = rows * kC4, teams = items >= 256 ? 1 : 256 / items;
+        // The last piece joins them all in range order: `teams` of threads (one
+        // for up to four pieces) take every teams-th piece each, four at a
+        // time, and are joined in order.
+        const int items = rows * kC4, most = items >= 256 ? 1 : 256 / items, want = (hi - lo + 4) / 4;
+        const int teams = want < most ? want : most;
         for (int i0 = 0; i0 < items; i0 += 256) {
           const int team = teams > 1 ? tid / items : 0, i = i0 + (teams > 1 ? tid - team * items : tid);
           const int r = i / kC4, c = 4 * (i - r * kC4);
@@ -532,6 +534,7 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.R = S::kRows;
   p.w.by_g = Divisor(p.w.g);
   p.w.by_R = Divisor(p.w.R);
+  p.w.by_hk = Divisor(kv.Hkv);
   p.w.starts = starts;
   p.w.status = device_status_ptr();
   const int page = 1 << kv.page_shift;
@@ -546,7 +549,7 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   for (int which = 0; which < 2; ++which) {
     const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(page), S::kHalves, static_cast<cuuint64_t>(kv.n_pages) * kv.Hkv};
     const cuuint64_t strides[3] = {HD * 2, 128, static_cast<cuuint64_t>(page) * HD * 2};
-    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.box), 1, 1};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(p.box), S::kHalves, 1};
     if (enc(which ? &vm : &km, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, which ? kv.v : kv.k, dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)

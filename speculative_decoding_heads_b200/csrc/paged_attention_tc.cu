@@ -658,8 +658,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           __stcg(slot + slot_row, m);
           __stcg(slot + 2 * kGroup + slot_row, l);
         }
-        __threadfence();
-        arrive(&bar->group[w]);
+        arrive(&bar->group[w]);                // then one thread's release covers all of them
         if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
         int lo, hi;
         C::owners(pl, x, lo, hi);
@@ -671,7 +670,6 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         arrive(&bar->group[w]);
         if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
         if (bar->last[w]) {
-          __threadfence();
           const int row0 = s.two ? w * kGroup : 0;
           // Few rows or many pieces: more pieces at a time; else more rows.
           if (rows <= 16 || hi - lo >= 6) join_rows<HD, 2, 4>(p.w, pl, x.start, lo, hi, row0, row, rows, put);
@@ -788,6 +786,7 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.R = 2 * p.rows;
   p.w.by_g = Divisor(p.w.g);
   p.w.by_R = Divisor(p.w.R);
+  p.w.by_hk = Divisor(kv.Hkv);
   const int most = starts ? N : N / kv.B;                // tokens of one sequence
   p.q_tokens = tokens < most ? tokens : most;
   const int page = 1 << kv.page_shift;

@@ -52,7 +52,7 @@ struct Work {
   TreeDev t;               // T = 0: causal chunks
   int N, H, g;             // g = H / Hkv
   int R;                   // query rows per tile
-  Divisor by_g, by_R;
+  Divisor by_g, by_R, by_hk;
   const int32_t* starts;
   float* slots;            // 2 per CTA, at the start of the workspace
   unsigned* counters;      // kCounters per unit, zero between calls
@@ -188,7 +188,7 @@ struct Cut {
     if (W > 0 && units < C && __all_sync(0xffffffffu, tiles[0] <= 1 && tiles[1] <= 1)) {
       // sum_u ceil(blocks_u / each) <= W / each + units <= C
       const unsigned total = static_cast<unsigned>(W), each = (total + C - units - 1) / (C - units);
-      if (each <= total / C + 2) {
+      if (each <= 2 || static_cast<unsigned long long>(each - 2) * C <= total) {
         if (lane == 0) {
           p.each = each;
           p.begin = p.end = 0;
@@ -197,7 +197,7 @@ struct Cut {
         unsigned cnt[2], blk[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          blk[i] = static_cast<unsigned>(work[i]) / hk;
+          blk[i] = static_cast<int>(work[i]) / w.by_hk;
           cnt[i] = (blk[i] + each - 1) / each;            // CTAs of one unit
         }
         unsigned at = (cnt[0] + cnt[1]) * hk;             // CTAs before the next lane's sequences
@@ -241,7 +241,7 @@ struct Cut {
     const int src = __ffs(__ballot_sync(0xffffffffu, begin >= off && begin < ws)) - 1;
     const int i = begin >= off + work[0] ? 1 : 0;
     if (i) off += work[0];
-    const unsigned rem = begin - static_cast<unsigned>(off), per_head = static_cast<unsigned>(i ? work[1] : work[0]) / hk;
+    const unsigned rem = begin - static_cast<unsigned>(off), per_head = static_cast<int>(i ? work[1] : work[0]) / w.by_hk;
     const unsigned head = per_head > 0 ? rem / per_head : 0u;
     const unsigned at = __shfl_sync(0xffffffffu, rem - head * per_head, src);
     const int Li = __shfl_sync(0xffffffffu, i ? L[1] : L[0], src), ni = __shfl_sync(0xffffffffu, i ? n[1] : n[0], src);
