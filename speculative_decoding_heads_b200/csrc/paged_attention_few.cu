@@ -104,15 +104,15 @@ __device__ void run_loads(const CUtensorMap* k_map, const CUtensorMap* v_map, co
   const int shift = p.w.kv.page_shift, mask = (1 << shift) - 1;
   const int none = p.w.kv.n_pages * p.w.kv.Hkv;        // past the last page block: reads as zeros
   int e = 0;
-  auto lookup = [&](int b, int h, int kb, int keys) {
+  auto lookup = [&](int b, int kb, int keys) {
     const int j = kb * kBK + lane * p.box;
-    if (lane >= sub || j >= keys) return none;
-    const int page = p.w.kv.table[static_cast<long long>(b) * p.w.kv.max_pages + (j >> shift)];
-    if (page < 0 || page >= p.w.kv.n_pages) {
-      set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
-      return none;
-    }
-    return page * p.w.kv.Hkv + h;
+    return lane < sub && j < keys ? p.w.kv.table[static_cast<long long>(b) * p.w.kv.max_pages + (j >> shift)] : kNoPage;
+  };
+  // The block (page, head) of a table entry, when its copy is issued: until then the entry is on its way.
+  auto block_of = [&](int page, int h) {
+    if (page >= 0 && page < p.w.kv.n_pages) return page * p.w.kv.Hkv + h;
+    if (page != kNoPage) set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
+    return none;
   };
   auto entry = [&](const CUtensorMap* map, int kb, int block) {
     const int st = e % S::kStages;
@@ -129,10 +129,11 @@ __device__ void run_loads(const CUtensorMap* k_map, const CUtensorMap* v_map, co
   };
   for (bool ok = true; ok;) {
     const int keys = C::keys(p.w, pl, x.b, x.tile);
-    int cur = lookup(x.b, x.h, x.kb0, keys);
+    int cur = lookup(x.b, x.kb0, keys);
     for (int kb = x.kb0; ok && kb < x.kb1; ++kb) {
-      const int next = kb + 1 < x.kb1 ? lookup(x.b, x.h, kb + 1, keys) : none;
-      ok = entry(k_map, kb, cur) && entry(v_map, kb, cur);
+      const int next = kb + 1 < x.kb1 ? lookup(x.b, kb + 1, keys) : kNoPage;
+      const int block = block_of(cur, x.h);
+      ok = entry(k_map, kb, block) && entry(v_map, kb, block);
       cur = next;
     }
     if (!ok || left == 0) break;

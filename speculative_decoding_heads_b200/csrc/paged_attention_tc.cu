@@ -150,16 +150,16 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
   const int shift = p.w.kv.page_shift, mask = (1 << shift) - 1;
   const int none = p.w.kv.n_pages * p.w.kv.Hkv;        // past the last page block: reads as zeros
   int e = 0, nq[2] = {0, 0};
-  // Block index (page, head) of this lane's box of key tile kb.
-  auto lookup = [&](int b, int h, int kb, int keys) {
+  // Table entry of this lane's box of key tile kb.
+  auto lookup = [&](int b, int kb, int keys) {
     const int j = kb * kBK + lane * p.box;
-    if (lane >= sub || j >= keys) return none;
-    const int page = p.w.kv.table[static_cast<long long>(b) * p.w.kv.max_pages + (j >> shift)];
-    if (page < 0 || page >= p.w.kv.n_pages) {
-      set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
-      return none;
-    }
-    return page * p.w.kv.Hkv + h;
+    return lane < sub && j < keys ? p.w.kv.table[static_cast<long long>(b) * p.w.kv.max_pages + (j >> shift)] : kNoPage;
+  };
+  // The block (page, head) of a table entry, when its copy is issued: until then the entry is on its way.
+  auto block_of = [&](int page, int h) {
+    if (page >= 0 && page < p.w.kv.n_pages) return page * p.w.kv.Hkv + h;
+    if (page != kNoPage) set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
+    return none;
   };
   auto entry = [&](const CUtensorMap* map, int kb, int block) {
     const int st = e % S::kStages;
@@ -189,17 +189,17 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
   for (bool ok = true; ok;) {
     const Seg s = segment(p, pl, x);
     const int keys = C::keys(p.w, pl, x.b, x.tile);
-    int cur = lookup(x.b, x.h, x.kb0, keys), next = s.n > 1 ? lookup(x.b, x.h, x.kb0 + 1, keys) : none;
+    int cur = lookup(x.b, x.kb0, keys), next = s.n > 1 ? lookup(x.b, x.kb0 + 1, keys) : kNoPage;
     ok = query(0, x.b, x.h, x.tile * p.w.R) && (!s.two || query(1, x.b, x.h, x.tile * p.w.R + p.rows));
-    ok = ok && entry(k_map, x.kb0, cur);
-    if (!s.two && s.n > 1) ok = ok && entry(k_map, x.kb0 + 1, next);
+    ok = ok && entry(k_map, x.kb0, block_of(cur, x.h));
+    if (!s.two && s.n > 1) ok = ok && entry(k_map, x.kb0 + 1, block_of(next, x.h));
     for (int i = 0; ok && i < s.n; ++i) {
-      const int after = i + 2 < s.n ? lookup(x.b, x.h, x.kb0 + i + 2, keys) : none;
-      ok = entry(v_map, x.kb0 + i, cur);
+      const int after = i + 2 < s.n ? lookup(x.b, x.kb0 + i + 2, keys) : kNoPage;
+      ok = entry(v_map, x.kb0 + i, block_of(cur, x.h));
       if (s.two) {
-        if (ok && i + 1 < s.n) ok = entry(k_map, x.kb0 + i + 1, next);
+        if (ok && i + 1 < s.n) ok = entry(k_map, x.kb0 + i + 1, block_of(next, x.h));
       } else if (ok && i + 2 < s.n) {
-        ok = entry(k_map, x.kb0 + i + 2, after);
+        ok = entry(k_map, x.kb0 + i + 2, block_of(after, x.h));
       }
       cur = next;
       next = after;

@@ -23,12 +23,15 @@
 // its slope), so neither the total nor a CTA's start needs a walk over tiles.
 #pragma once
 
+#include <climits>
+
 #include "common.cuh"
 
 namespace medusa {
 namespace paged {
 
 constexpr int kCounters = 2;   // per unit: row groups that are joined on their own
+constexpr int kNoPage = INT_MIN;   // in place of a table entry: nothing to look up
 
 // x / d for 0 <= x < 2^31 and 1 <= d <= 2^15 as one product: with 2^k >= d and
 // m = ceil(2^(31+k) / d), x m / 2^(31+k) exceeds x / d by less than 2^-k <= 1/d.
