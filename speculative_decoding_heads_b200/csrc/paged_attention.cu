@@ -240,28 +240,59 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
       __syncthreads();
       write = s_last != 0;
       if (write) {
+        // kPB pieces' loads (from L2) in flight together: one after the other they took as long as a block.
+        constexpr int kPB = RR * DV <= 4 ? 4 : RR * DV <= 8 ? 2 : 1;
 #pragma unroll
         for (int r = 0; r < RR; ++r) {
-          const int row = ty * RR + r;
           m[r] = -INFINITY;
-          for (int c = c_lo; c <= c_hi; ++c) m[r] = fmaxf(m[r], __ldcg(w.slots + C::slot(plan, c, x.start) * slot_floats(R, HD) + row));
           l[r] = 0.f;
 #pragma unroll
           for (int d = 0; d < DV; ++d)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[r][d][e] = 0.f;
-          const float ref = m[r] == -INFINITY ? 0.f : m[r];
-          for (int c = c_lo; c <= c_hi; ++c) {
-            const float* sl = w.slots + C::slot(plan, c, x.start) * slot_floats(R, HD);
-            const float f = exp2f(__ldcg(sl + row) - ref);
-            l[r] += f * __ldcg(sl + R + row);
+        }
+#pragma unroll 1
+        for (int c0 = c_lo; c0 <= c_hi; c0 += kPB) {
+          float ms[RR][kPB], ls[RR][kPB];
+          float4 v[RR][kPB][DV];
 #pragma unroll
-            for (int d = 0; d < DV; ++d) {
-              const float4 v = __ldcg(reinterpret_cast<const float4*>(sl + 2 * R + row * HD + 64 * d + 4 * tx));
-              o[r][d][0] = fmaf(f, v.x, o[r][d][0]);
-              o[r][d][1] = fmaf(f, v.y, o[r][d][1]);
-              o[r][d][2] = fmaf(f, v.z, o[r][d][2]);
-              o[r][d][3] = fmaf(f, v.w, o[r][d][3]);
+          for (int c = 0; c < kPB; ++c) {
+            const float* sl = w.slots + C::slot(plan, min(c0 + c, c_hi), x.start) * slot_floats(R, HD);
+#pragma unroll
+            for (int r = 0; r < RR; ++r) {
+              const int row = ty * RR + r;
+              const bool have = c0 + c <= c_hi;
+              ms[r][c] = have ? __ldcg(sl + row) : -INFINITY;
+              ls[r][c] = have ? __ldcg(sl + R + row) : 0.f;
+#pragma unroll
+              for (int d = 0; d < DV; ++d)
+                v[r][c][d] = have ? __ldcg(reinterpret_cast<const float4*>(sl + 2 * R + row * HD + 64 * d + 4 * tx))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+          }
+#pragma unroll
+          for (int r = 0; r < RR; ++r) {
+            float mn = m[r];
+#pragma unroll
+            for (int c = 0; c < kPB; ++c) mn = fmaxf(mn, ms[r][c]);
+            const float ref = mn == -INFINITY ? 0.f : mn, keep = exp2f(m[r] - ref);
+            m[r] = mn;
+            l[r] *= keep;
+#pragma unroll
+            for (int d = 0; d < DV; ++d)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[r][d][e] *= keep;
+#pragma unroll
+            for (int c = 0; c < kPB; ++c) {
+              const float f = exp2f(ms[r][c] - ref);
+              l[r] = fmaf(f, ls[r][c], l[r]);
+#pragma unroll
+              for (int d = 0; d < DV; ++d) {
+                o[r][d][0] = fmaf(f, v[r][c][d].x, o[r][d][0]);
+                o[r][d][1] = fmaf(f, v[r][c][d].y, o[r][d][1]);
+                o[r][d][2] = fmaf(f, v[r][c][d].z, o[r][d][2]);
+                o[r][d][3] = fmaf(f, v[r][c][d].w, o[r][d][3]);
+              }
             }
           }
         }
