@@ -5,13 +5,20 @@
 // One pass over the keys with a running maximum and sum per query row: with
 // m' = max(m, max_j s_j), O <- O 2^(m - m') + sum_j 2^(s_j - m') V_j and the
 // same for the sum l, the output is O / l whatever the order of the blocks.
-// A CTA holds R query rows and takes 64 keys at a time through shared memory
-// as fp32; a thread owns R / 16 or R / 8 rows x 4 keys of the scores and the
-// same rows x HD / 16 dimensions of O, so one 16-byte shared-memory read
-// feeds 16 products.  The probabilities take the place of the keys, which
-// leaves room for two CTAs per SM at 128 dimensions: one computes while the
-// other's loads are in flight.  R = 16 where the largest chunk fits (decoding and small
-// trees, bound by the cache's bytes), 64 otherwise (bound by fp32 arithmetic).
+// A CTA holds R query rows and takes 32 or 64 keys at a time through shared
+// memory as fp32; a thread owns R / 16 or R / 8 rows x 2 or 4 keys of the
+// scores and the same rows x HD / 16 dimensions of O, so one 16-byte
+// shared-memory read feeds 8 to 16 products.  The probabilities take the place
+// of the keys, which leaves room for more CTAs per SM: some compute while the
+// others' loads are in flight.
+//
+// R = 16 where a sequence's rows fit (decoding and small trees): bound by the
+// latency of a block's loads, products and barriers, hence blocks of 32 keys,
+// four or five CTAs per SM, and warps without a row that only load (4 tokens
+// of 32 fp32 heads over 2721 rows 108 us, 3.3 TB/s; blocks of 64 keys, two
+// CTAs and every warp computing took 263).  R = 64 otherwise, bound by fp32
+// arithmetic and its shared-memory reads (4 x 257 tokens of the same heads
+// 1.78 ms, 27 TFLOP/s).
 #include "paged_work.cuh"
 
 namespace medusa {
@@ -19,7 +26,6 @@ namespace {
 
 using namespace paged;
 
-constexpr int kBK = 64;          // keys per block
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <typename T>
@@ -40,13 +46,14 @@ __device__ __forceinline__ void store4(uint16_t* p, float4 v) {
 
 template <int HD, int R>
 struct Shape {
+  static constexpr int kBK = R == 16 ? 32 : 64;       // keys per block
   static constexpr int kRows = R == 16 ? 2 : 4;       // query rows per thread
   static constexpr int kThreads = R / kRows * 16;     // 16 threads side by side per row group
   static constexpr int kPitch = HD + 4;               // floats per row: conflict-free 16-byte reads down a column
   static constexpr int kPPitch = kBK + 4;
   static_assert(R * kPPitch <= kBK * kPitch, "the probabilities take the place of the keys");
   static constexpr size_t kSmem = static_cast<size_t>(R + 2 * kBK) * kPitch * sizeof(float);
-  static constexpr int kPerSm = kSmem > 112 * 1024 ? 1 : kSmem > 74 * 1024 || R == 64 ? 2 : 3;
+  static constexpr int kPerSm = kSmem > 112 * 1024 ? 1 : kSmem > 74 * 1024 || R == 64 ? 2 : HD == 128 ? 4 : 5;
   static constexpr int kLoads = kBK * (HD / 4) / kThreads;   // four-element loads of K, and of V, per thread and block
   static constexpr int kBatch = kLoads < 8 ? kLoads : 8;     // in flight together
   static_assert(2 * kPerSm * slot_floats(R, HD) <= kSlotFloatsPerSm, "two slots per CTA");
@@ -54,8 +61,9 @@ struct Shape {
 };
 
 template <typename T, int HD, int R>
-__global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(const Work w, const T* q, float scale_log2, T* out) {
+__global__ void __launch_bounds__(Shape<HD, R>::kThreads, Shape<HD, R>::kPerSm) paged_attn_kernel(const Work w, const T* q, float scale_log2, T* out) {
   using S = Shape<HD, R>;
+  constexpr int kBK = S::kBK, KC = kBK / 16;       // KC keys per thread
   using C = Cut<kBK>;
   constexpr int NT = S::kThreads, RR = S::kRows, DV = HD / 64;   // DV groups of 4 dimensions per thread
   extern __shared__ __align__(16) float sh[];
@@ -76,6 +84,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
   for (;;) {
     const int b = x.b, L = plan.L[b], n = plan.n[b], first = plan.first[b];
     const int rows = min(R, n * g - x.tile * R);
+    const bool mine = R > 16 || (ty & ~1) * RR < rows;     // this warp has rows
     const int keys = C::keys(w, plan, b, x.tile);
     __syncthreads();                       // the piece before is done with shared memory
     for (int i = tid; i < R * (HD / 4); i += NT) {
@@ -105,7 +114,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
 #pragma unroll 1
       for (int base = 0; base < S::kLoads; base += S::kBatch) {
         long long off[S::kBatch];
-        float4 t[S::kBatch];
+        float4 tk[S::kBatch], tv[S::kBatch];
 #pragma unroll
         for (int u = 0; u < S::kBatch; ++u) {
           const int i = tid + (base + u) * NT, r = i / (HD / 4), d = i - r * (HD / 4);
@@ -118,38 +127,45 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
               set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedPage);
           }
         }
-        auto fetch = [&](const void* from, float* to) {
+        auto fetch = [&](const void* from, float4 (&t)[S::kBatch]) {
 #pragma unroll
           for (int u = 0; u < S::kBatch; ++u) t[u] = off[u] >= 0 ? load4<T>(static_cast<const T*>(from) + off[u]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        auto put = [&](const float4 (&t)[S::kBatch], float* to) {
 #pragma unroll
           for (int u = 0; u < S::kBatch; ++u) {
             const int i = tid + (base + u) * NT, r = i / (HD / 4), d = i - r * (HD / 4);
             *reinterpret_cast<float4*>(to + r * S::kPitch + 4 * d) = t[u];
           }
         };
-        fetch(w.kv.k, ks);
-        fetch(w.kv.v, vs);
+        fetch(w.kv.k, tk);
+        fetch(w.kv.v, tv);
+        put(tk, ks);
+        put(tv, vs);
       }
       __syncthreads();
-      float s[RR][4];
-#pragma unroll
-      for (int r = 0; r < RR; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s[r][c] = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < HD / 4; ++d) {
-        float4 a[RR], k4[4];
-#pragma unroll
-        for (int r = 0; r < RR; ++r) a[r] = *reinterpret_cast<const float4*>(qs + (ty * RR + r) * S::kPitch + 4 * d);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) k4[c] = *reinterpret_cast<const float4*>(ks + (tx + 16 * c) * S::kPitch + 4 * d);
+      float s[RR][KC];
+      if (mine) {
 #pragma unroll
         for (int r = 0; r < RR; ++r)
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            s[r][c] = fmaf(a[r].x, k4[c].x, fmaf(a[r].y, k4[c].y, fmaf(a[r].z, k4[c].z, fmaf(a[r].w, k4[c].w, s[r][c]))));
+          for (int c = 0; c < KC; ++c) s[r][c] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < HD / 4; ++d) {
+          float4 a[RR], k4[KC];
+#pragma unroll
+          for (int r = 0; r < RR; ++r) a[r] = *reinterpret_cast<const float4*>(qs + (ty * RR + r) * S::kPitch + 4 * d);
+#pragma unroll
+          for (int c = 0; c < KC; ++c) k4[c] = *reinterpret_cast<const float4*>(ks + (tx + 16 * c) * S::kPitch + 4 * d);
+#pragma unroll
+          for (int r = 0; r < RR; ++r)
+#pragma unroll
+            for (int c = 0; c < KC; ++c)
+              s[r][c] = fmaf(a[r].x, k4[c].x, fmaf(a[r].y, k4[c].y, fmaf(a[r].z, k4[c].z, fmaf(a[r].w, k4[c].w, s[r][c]))));
+        }
       }
       __syncthreads();                     // P goes where K was
+      if (!mine) continue;
 #pragma unroll
       for (int r = 0; r < RR; ++r) {
         const int rr = x.tile * R + ty * RR + r, tok = rr / w.by_g;
@@ -163,7 +179,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
           sees = o < 0 ? w0 << sh | ((1ull << sh) - 1ull) : sh == 0 ? w0 : (w0 >> sh) | (w1 << (64 - sh));
         }
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < KC; ++c) {
           const int j = j0 + tx + 16 * c, rel = j - L;
           bool see;
           if (w.t.T > 0)
@@ -178,7 +194,7 @@ __global__ void __launch_bounds__(Shape<HD, R>::kThreads) paged_attn_kernel(cons
         const float f = exp2f(m[r] - ref);
         float sum = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < KC; ++c) {
           const float p = exp2f(s[r][c] - ref);
           ps[(ty * RR + r) * S::kPPitch + tx + 16 * c] = p;
           sum += p;
