@@ -428,6 +428,8 @@ LOGITS = [
     (2, 6000, (2, 2, 6), None, "rf"),
     (5, 2052, (3, 2, 14), [9, 1, 0, 2, 400], "p"),
     (1, 300, (2, 2, 6), [5], ""),
+    (64, 20_003, (1, 1, 0), [(37 * b) % 900 for b in range(64)], "rpfbm"),    # single tokens, several chunks to a block
+    (33, 65_536, (1, 1, 0), [40] * 33, "rpfm"),
 ]
 
 
