@@ -13,7 +13,11 @@
 // P enters the second product as a bf16 pair (high part and remainder), whose
 // second multiplication is free here: the output is rounded once, to bf16.
 // The maximum is moved only when it grows by more than 2^8, as in
-// paged_attention_tc.cu, whose ring and TMA boxes these loads share.
+// paged_attention_tc.cu.
+//
+// Measured: 13 tokens of 40 heads in groups of 5 over 4099..60001 rows 255 us,
+// 6.7 TB/s; one token of 32 heads over 1024 rows in pages of 16 10.9 us, all
+// of it latency (plan, page ids, three tiles of eight copies each, join).
 #include <cudaTypedefs.h>
 
 #include "paged_work.cuh"
@@ -569,12 +573,18 @@ long long most_rows(const PagedDev& kv, int N, int H, const int32_t* starts) {
 
 }  // namespace
 
-// Up to 16 rows: 29 sequences of 40 heads and 467..1515 rows took 129, 134 and
-// 158 us with 1, 8 and 16 rows (128-row products: 140, 139, 137), one of 32
-// heads and 1024 rows 12.6, 12.1 and 13.7 (14.6, 14.7, 15.0), heads of 64 98,
-// 103 and 109 (127, 119, 121).  17 rows would double the products: 395.
+// Up to 16 rows.  Against 128-row products, with 1, 8 and 16 rows: one sequence
+// of 32 heads over 1024 rows 11.1, 11.3 and 12.6 us (13.2, 13.3, 13.5), 8 of 32
+// over 4000 85.9, 87.2 (4 rows) and 90.5 (89.1, 90.0, 90.2), 29 of 40 heads of
+// 64 over 467..1515 87.7, 92.7 and 99.9 (113, 108, 104).  Many short units of
+// heads of 128 pay for every row in the join of the eight warps: 29 sequences
+// of 40 heads take 118.5, 121.5, 125, 126.5 and 143.5 us with 2, 4, 6, 8 and 16
+// rows (119.5, 121, 122, 115, 114), so those with more than four rows go to
+// the other kernel.  17 rows would double the products here: 395 us.
 bool paged_attention_few_supported(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const int32_t* starts) {
-  return dtype == MEDUSA_BF16 && (kv.hd == 64 || kv.hd == 128) && most_rows(kv, N, H, starts) <= 16 &&
+  const long long rows = most_rows(kv, N, H, starts);
+  const bool many_units = kv.B * kv.Hkv > 4 * sm_count();
+  return dtype == MEDUSA_BF16 && (kv.hd == 64 || kv.hd == 128) && rows <= (many_units && kv.hd == 128 ? 4 : 16) &&
          static_cast<long long>(kv.n_pages) * kv.Hkv < 0x7fffffffll;
 }
 

@@ -8,7 +8,10 @@
 // 2^-32 turns.  A block computes cos and sin once per (token, pair) into
 // shared memory for all H + Hkv heads.
 //
-// Bound by HBM: every element is read once and written once.
+// Bound by HBM: every element is read once and written once (8445 tokens of
+// 32 + 2 x 8 heads of 128 46 us, 4.5 TB/s; a plain copy of as many bytes takes
+// 35).  One wave of blocks, so that each sets up once: two to eight waves took
+// as long, a block per token 51 us.
 #include "common.cuh"
 
 namespace medusa {
