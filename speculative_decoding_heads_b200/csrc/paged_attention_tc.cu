@@ -776,6 +776,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Two groups to a unit read the keys once for both, but where that leaves fewer
+// units than SMs every unit is cut into pieces, and the SM that joins them
+// reads them all (32 bytes a clock): with one group there are twice as many
+// joins of half the size.  One group against two: two 64-node trees of 32 heads
+// over 2000 rows 23.8 us, 31.9; 100 tokens of 16 heads after 9000 rows 42.4,
+// 57.6; 256 and 1024 of 32 heads after 4000 rows 37.6 and 84, 45.2 and 86.
+int rows_per_unit(int N, int H, int rows) {
+  return static_cast<long long>(N) * H < 2ll * rows * sm_count() ? rows : 2 * rows;
+}
+
 template <int HD>
 medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float scale, const TreeDev* tree,
                        const int32_t* starts, void* out, void* ws, cudaStream_t stream) {
@@ -792,7 +802,7 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.status = device_status_ptr();
   const int tokens = kGroup / p.w.g;
   p.rows = tokens * p.w.g;
-  p.w.R = 2 * p.rows;
+  p.w.R = rows_per_unit(N, H, p.rows);
   p.w.by_g = Divisor(p.w.g);
   p.w.by_R = Divisor(p.w.R);
   p.w.by_hk = Divisor(kv.Hkv);
@@ -839,7 +849,7 @@ bool paged_attention_tc_supported(const PagedDev& kv, medusa_dtype_t dtype, int 
 
 size_t paged_attention_tc_workspace_bytes(const PagedDev& kv, int N, int H) {
   const int g = H / kv.Hkv;
-  return slots_bytes() + counter_bytes(N, H, kv.Hkv, kv.B, 2 * (kGroup / g) * g);
+  return slots_bytes() + counter_bytes(N, H, kv.Hkv, kv.B, rows_per_unit(N, H, kGroup / g * g));
 }
 
 medusa_status_t launch_paged_attention_tc(const PagedDev& kv, int N, int H, const void* q, float scale, const TreeDev* tree,

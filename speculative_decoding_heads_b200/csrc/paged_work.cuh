@@ -11,11 +11,13 @@
 // per unit and row group) joins them in range order, so the result does not
 // depend on who was last.
 //
-// Where every sequence is one tile and there are fewer units than CTAs (a few
-// requests decoding), a cut at unit boundaries is better: every unit gets a
-// whole number of CTAs, at most `each` blocks to each, and no CTA pays for two
-// pieces.  It is taken when it costs a CTA at most two blocks more than the
-// equal cut (the set-up and output of a second piece take about as long).
+// Where a sequence's units all cost the same (one tile, or a tree's) and there
+// are fewer units than CTAs (a few requests decoding), a cut at unit boundaries
+// is better: every unit gets a whole number of CTAs, at most `each` blocks to
+// each, and no CTA pays for two pieces.  It is taken when it costs a CTA at
+// most two blocks more than the equal cut (the set-up and output of a second
+// piece take about as long): one token of 32 heads over 1024 rows 10.9 us, cut
+// equally 13.0.
 //
 // One warp lays the plan, two sequences to a lane: the blocks of a sequence's
 // first t tiles, sum_{i=1..t} ceil((g L + i R) / (g BK)), have a closed form
@@ -188,7 +190,7 @@ struct Cut {
     }
     if (bad && blockIdx.x == 0) set_device_status(w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
     const unsigned c = blockIdx.x, C = gridDim.x, units = static_cast<unsigned>(both & 0x3ffffffu) * hk;
-    if (W > 0 && units < C && __all_sync(0xffffffffu, tiles[0] <= 1 && tiles[1] <= 1)) {
+    if (W > 0 && units < C && (w.t.T > 0 || __all_sync(0xffffffffu, tiles[0] <= 1 && tiles[1] <= 1))) {
       // sum_u ceil(blocks_u / each) <= W / each + units <= C
       const unsigned total = static_cast<unsigned>(W), each = (total + C - units - 1) / (C - units);
       if (each <= 2 || static_cast<unsigned long long>(each - 2) * C <= total) {
@@ -197,31 +199,33 @@ struct Cut {
           p.begin = p.end = 0;
         }
         __syncwarp();
-        unsigned cnt[2], blk[2];
+        unsigned cnt[2], blk[2], all[2];                  // a unit's CTAs and blocks, a sequence's CTAs
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           blk[i] = static_cast<int>(work[i]) / w.by_hk;
-          cnt[i] = (blk[i] + each - 1) / each;            // CTAs of one unit
+          if (tiles[i] > 1) blk[i] /= tiles[i];           // all of a tree's tiles see the same keys
+          cnt[i] = (blk[i] + each - 1) / each;
+          all[i] = cnt[i] * hk * tiles[i];
         }
-        unsigned at = (cnt[0] + cnt[1]) * hk;             // CTAs before the next lane's sequences
+        unsigned at = all[0] + all[1];                    // CTAs before the next lane's sequences
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
           const unsigned v = __shfl_up_sync(0xffffffffu, at, o);
           if (lane >= o) at += v;
         }
-        at -= (cnt[0] + cnt[1]) * hk;
-        const int i = c >= at + cnt[0] * hk ? 1 : 0;
-        if (i) at += cnt[0] * hk;
-        const unsigned k = i ? cnt[1] : cnt[0], nb = i ? blk[1] : blk[0];
-        if (c >= at && c < at + k * hk) {
-          const unsigned h = (c - at) / k, part = c - at - h * k;
+        at -= all[0] + all[1];
+        const int i = c >= at + all[0] ? 1 : 0;
+        if (i) at += all[0];
+        const unsigned k = i ? cnt[1] : cnt[0], nb = i ? blk[1] : blk[0], nt = i ? tiles[1] : tiles[0];
+        if (c >= at && c < at + (i ? all[1] : all[0])) {
+          const unsigned u = (c - at) / k, part = c - at - u * k, h = nt > 1 ? u / nt : u;
           p.b = 2 * lane + i;
           p.h = static_cast<int>(h);
-          p.tile = 0;
+          p.tile = static_cast<int>(u - h * nt);
           p.block = static_cast<int>(nb * part / k);
           p.end = nb * (part + 1) / k - p.block;
-          p.lo = static_cast<int>(at + h * k);
-          p.hi = static_cast<int>(at + h * k + k - 1);
+          p.lo = static_cast<int>(at + u * k);
+          p.hi = static_cast<int>(at + u * k + k - 1);
         }
         return;
       }

@@ -222,6 +222,10 @@ ATTN = [
     ("bf16", 128, 64, 3, 1, [511], [129]),
     ("bf16", 128, 64, 32, 2, [63], [9]),
     ("bf16", 128, 64, 8, 2, [300], [2048]),      # many tiles to a CTA, whole ones and pieces, one key tile and more
+    ("bf16", 128, 64, 64, 8, [300, 40], [500, 140]),      # from here to 63 heads: enough rows for two groups to a unit
+    ("bf16", 64, 32, 64, 8, [0, 130], [303, 300]),
+    ("bf16", 128, 64, 32, 8, [300, 0, 90], [1300, 1, 30]),
+    ("bf16", 128, 16, 63, 9, [1, 500], [600, 50]),
     ("bf16", 64, 16, 4, 2, [100, 5], [3, 140]),
     ("bf16", 64, 64, 9, 3, [1500, 3], [1, 1]),
     ("bf16", 96, 16, 2, 2, [70], [20]),
@@ -249,6 +253,9 @@ TREES = [
     ("bf16", 128, 16, 1, 1, [77], 5, 10, 255),
     ("bf16", 64, 8, 8, 2, [40], 4, 8, 48),
     ("bf16", 128, 16, 4, 4, [50], 1, 1, 0),
+    ("bf16", 128, 64, 8, 1, [700, 2], 5, 10, 63),          # several tiles of one key head
+    ("bf16", 64, 16, 20, 2, [300, 90, 0], 5, 10, 100),
+    ("bf16", 128, 64, 64, 4, [260, 70, 31], 5, 10, 254),   # enough rows for two groups to a unit
     ("f32", 64, 16, 4, 4, [64, 5], 3, 2, 14),
     ("f32", 128, 64, 2, 1, [130], 5, 10, 64),
 ]
