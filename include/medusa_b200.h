@@ -522,7 +522,7 @@ typedef struct medusa_paged_kv {
  * does a page id outside [0, n_pages) for the rows in that page (where
  * attention reads such a page, its keys and values count as zeros).
  * chunk_starts that descend set it too, and attention then computes nothing;
- * so does attention over more than 2^31 blocks of keys in one call.
+ * so does attention over more than 2^30 blocks of keys in one call.
  * 1 <= N <= 2^22, 1 <= H <= 256. */
 
 typedef enum medusa_rope_layout {

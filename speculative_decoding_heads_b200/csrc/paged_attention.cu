@@ -409,6 +409,7 @@ medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype,
   w.by_R = Divisor(w.R);
   w.by_hk = Divisor(kv.Hkv);
   w.join = c.R == 16 ? 0.03f : 0.02f;
+  w.extra = c.R == 16 ? 1u : 0u;
   w.slots = static_cast<float*>(ws);
   w.counters = counters_of(ws);
   const int grid = sm_count() * c.per_sm;

@@ -541,6 +541,7 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.by_R = Divisor(p.w.R);
   p.w.by_hk = Divisor(kv.Hkv);
   p.w.join = 0.15f;
+  p.w.extra = 2u;
   p.w.starts = starts;
   p.w.status = device_status_ptr();
   const int page = 1 << kv.page_shift;

@@ -807,6 +807,7 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.by_R = Divisor(p.w.R);
   p.w.by_hk = Divisor(kv.Hkv);
   p.w.join = 1.5f;
+  p.w.extra = 2u;
   const int most = starts ? N : N / kv.B;                // tokens of one sequence
   p.q_tokens = tokens < most ? tokens : most;
   const int page = 1 << kv.page_shift;

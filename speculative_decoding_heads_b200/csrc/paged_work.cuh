@@ -59,6 +59,7 @@ struct Work {
   int R;                   // query rows per tile
   Divisor by_g, by_R, by_hk;
   float join;              // joining one piece of a unit, in units of computing one block
+  unsigned extra;          // blocks that a unit's set-up and output cost besides its own
   const int32_t* starts;
   float* slots;            // 2 per CTA, at the start of the workspace
   unsigned* counters;      // kCounters per unit, zero between calls
@@ -68,6 +69,7 @@ struct Work {
 struct Plan {
   int L[MEDUSA_MAX_B], n[MEDUSA_MAX_B], first[MEDUSA_MAX_B];
   unsigned each;                       // cut at unit boundaries: blocks per CTA; 0: equal ranges
+  unsigned extra;                      // equal ranges: Work::extra, otherwise 0
   unsigned per, more;                  // equal ranges: blocks of a CTA, and how many of the first hold one more
   unsigned begin, end;                 // this CTA's range
   int b, h, tile, block;               // where it starts
@@ -183,9 +185,10 @@ struct Cut {
       if (lane >= o) both += v;
     }
     const unsigned long long ws = both >> 26;
+    const unsigned upto = static_cast<unsigned>(both & 0x3ffffffu);   // tiles, this lane's included
     both = __shfl_sync(0xffffffffu, both, 31);
     unsigned long long W = both >> 26;
-    if (W > 0x7fffffffull) {     // 2^31 blocks of keys in one call: refused like any other impossible chunk
+    if (W > 0x3fffffffull) {     // 2^30 blocks of keys in one call: refused like any other impossible chunk
       W = 0;
       bad = true;
     }
@@ -205,6 +208,7 @@ struct Cut {
         each = max(each, least);
         if (lane == 0) {
           p.each = each;
+          p.extra = 0u;
           p.begin = p.end = 0;
         }
         __syncwarp();
@@ -240,21 +244,27 @@ struct Cut {
       }
     }
     // No more ranges than blocks, so that none is empty.
-    const unsigned fit = max(1u, static_cast<unsigned>(W) / least), r = W == 0 ? 0u : min(fit, C), per = r > 0 ? static_cast<unsigned>(W) / r : 0u;
-    const unsigned more = static_cast<unsigned>(W) - per * r;
+    const unsigned fit = max(1u, static_cast<unsigned>(W) / least), r = W == 0 ? 0u : min(fit, C);
+    // Every unit is followed by its extra blocks, which nobody computes.
+    const unsigned all = static_cast<unsigned>(W) + (W == 0 ? 0u : w.extra * units), per = r > 0 ? all / r : 0u;
+    const unsigned more = all - per * r;
     const unsigned begin = c < r ? range_begin(c, per, more) : 0u;
     const unsigned end = c < r ? range_begin(c + 1, per, more) : 0u;
     if (lane == 0) {
       p.per = per;
       p.more = more;
       p.each = 0u;
+      p.extra = w.extra;
       p.begin = begin;
       p.end = end;
     }
     if (begin >= end) return;
     // The lane whose sequences hold offset begin, and where in them it lies.
-    unsigned long long off = ws - work[0] - work[1];      // blocks before this lane's sequences
-    const int src = __ffs(__ballot_sync(0xffffffffu, begin >= off && begin < ws)) - 1;
+    work[0] += w.extra * hk * tiles[0];
+    work[1] += w.extra * hk * tiles[1];
+    const unsigned long long to = ws + w.extra * hk * upto, from = to - work[0] - work[1];
+    unsigned long long off = from;                        // blocks before this lane's sequences
+    const int src = __ffs(__ballot_sync(0xffffffffu, begin >= from && begin < to)) - 1;
     const int i = begin >= off + work[0] ? 1 : 0;
     if (i) off += work[0];
     const unsigned rem = begin - static_cast<unsigned>(off), per_head = static_cast<int>(i ? work[1] : work[0]) / w.by_hk;
@@ -269,16 +279,29 @@ struct Cut {
     while (step * 32 < nt) step *= 32;
     for (; nt > 1 && step > 0; step /= 32) {
       const long long t = lo + static_cast<long long>(lane) * step;
-      const unsigned long long s = t < nt ? before_tile(w, Li, ni, nt, static_cast<int>(t)) : ~0ull;
+      const unsigned long long s = t < nt ? before_tile(w, Li, ni, nt, static_cast<int>(t)) + w.extra * static_cast<unsigned>(t) : ~0ull;
       const int k = 31 - __clz(__ballot_sync(0xffffffffu, s <= at));   // lane 0's always is
       lo += k * step;
       at_lo = __shfl_sync(0xffffffffu, static_cast<unsigned>(s), k);
     }
+    __syncwarp();              // the lengths of all sequences, and lane 0's begin and end
     if (lane == src) {
-      p.b = 2 * lane + i;
-      p.h = static_cast<int>(head);
-      p.tile = lo;
-      p.block = static_cast<int>(at - at_lo);
+      Piece x;
+      x.b = 2 * lane + i;
+      x.h = static_cast<int>(head);
+      x.tile = lo;
+      int block = static_cast<int>(at - at_lo);
+      const int own = blocks(w, p, x.b, lo);
+      if (block >= own) {      // behind a unit's own blocks: the next unit's, if the range reaches it
+        const unsigned skip = own + w.extra - block;
+        p.begin = end - begin > skip ? begin + skip : end;
+        block = 0;
+        if (end - begin > skip) next_unit(w, p, x);
+      }
+      p.b = x.b;
+      p.h = x.h;
+      p.tile = x.tile;
+      p.block = block;
     }
   }
 
@@ -306,27 +329,30 @@ struct Cut {
     x.kb0 = p.block;
     x.start = p.begin - p.block;
     x.blocks = blocks(w, p, x.b, x.tile);
-    take(x, left);
+    take(p, x, left);
     return x;
   }
   static __device__ __forceinline__ void next_piece(const Work& w, const Plan& p, Piece& x, unsigned& left) {
-    x.start += x.blocks;
+    x.start += x.blocks + p.extra;
     x.kb0 = 0;
+    next_unit(w, p, x);
+    x.blocks = blocks(w, p, x.b, x.tile);
+    take(p, x, left);
+  }
+  static __device__ __forceinline__ void next_unit(const Work& w, const Plan& p, Piece& x) {
     if (++x.tile == tiles_of(w, p.n[x.b])) {
       x.tile = 0;
       if (++x.h == w.kv.Hkv) {
         x.h = 0;
-        do ++x.b; while (p.n[x.b] == 0);     // left > 0, so there is one
+        do ++x.b; while (p.n[x.b] == 0);     // blocks are left, so there is one
       }
     }
-    x.blocks = blocks(w, p, x.b, x.tile);
-    take(x, left);
   }
-  static __device__ __forceinline__ void take(Piece& x, unsigned& left) {
+  static __device__ __forceinline__ void take(const Plan& p, Piece& x, unsigned& left) {
     const unsigned room = static_cast<unsigned>(x.blocks - x.kb0);
-    const unsigned m = room < left ? room : left;
+    const unsigned m = room < left ? room : left, used = m == room ? room + p.extra : m;
     x.kb1 = x.kb0 + static_cast<int>(m);
-    left -= m;
+    left = left > used ? left - used : 0u;
   }
   static __device__ __forceinline__ bool whole(const Piece& x) { return x.kb0 == 0 && x.kb1 == x.blocks; }
 
