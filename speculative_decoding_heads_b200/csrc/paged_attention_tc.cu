@@ -807,7 +807,7 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.by_R = Divisor(p.w.R);
   p.w.by_hk = Divisor(kv.Hkv);
   p.w.join = 1.5f;
-  p.w.extra = 2u;
+  p.w.extra = 3u;          // 6000 clocks between units, 1900 a block: 26 prompts of 75..865 tokens 83 us (0: 90, 6: 89)
   const int most = starts ? N : N / kv.B;                // tokens of one sequence
   p.q_tokens = tokens < most ? tokens : most;
   const int page = 1 << kv.page_shift;

@@ -5,7 +5,9 @@
 // see.  All units' blocks, laid end to end in (sequence, key head, tile)
 // order, are cut into one equal range per CTA, so that a few long sequences
 // fill the GPU as well as many short ones, with nothing decided on the host
-// (the lengths are device memory).  A unit that a range boundary cuts is
+// (the lengths are device memory).  Behind every unit come a few blocks that
+// nobody computes: its set-up and output cost as much, and a CTA with many
+// short units gets fewer blocks.  A unit that a range boundary cuts is
 // computed in pieces: each piece leaves its unnormalised output, row maxima
 // and row sums in the CTA's slot, and the piece that finishes last (a counter
 // per unit and row group) joins them in range order, so the result does not
