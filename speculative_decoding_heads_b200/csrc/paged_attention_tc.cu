@@ -706,57 +706,59 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* bar = reinterpret_cast<Bars*>(smem + S::kOffBars);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // Registers: launched with 168 a thread; the softmax warpgroups take what the others give up
-  // (128 * 104 + 256 * 200 = 384 * 168).
-  if (warp == 0) {
+  // (128 * 104 + 256 * 200 = 384 * 168).  A warpgroup's threads all execute the same setmaxnreg, which
+  // the instruction demands: the branch that holds it is a warpgroup's, and roles part behind it.
+  if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (lane == 0) {
-      for (int st = 0; st < S::kStages; ++st) {
-        mbar_init(&bar->full[st], 1);
-        mbar_init(&bar->empty[st], 1);
+    if (warp == 0) {
+      if (lane == 0) {
+        for (int st = 0; st < S::kStages; ++st) {
+          mbar_init(&bar->full[st], 1);
+          mbar_init(&bar->empty[st], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+          mbar_init(&bar->q_full[w], 1);
+          mbar_init(&bar->q_empty[w], 1);
+          mbar_init(&bar->s_full[w], 1);
+          mbar_init(&bar->p_half[w], 4);
+          mbar_init(&bar->p_full[w], 4);
+          mbar_init(&bar->pv_done[w], 1);
+          mbar_init(&bar->o_free[w], 4);
+          mbar_init(&bar->group[w], 4);
+        }
+        mbar_init(&bar->stat_full, 4);
+        mbar_init(&bar->stat_free, 4);
+        bar->abort = 0;
+        fence_barrier_init();
       }
-      for (int w = 0; w < 2; ++w) {
-        mbar_init(&bar->q_full[w], 1);
-        mbar_init(&bar->q_empty[w], 1);
-        mbar_init(&bar->s_full[w], 1);
-        mbar_init(&bar->p_half[w], 4);
-        mbar_init(&bar->p_full[w], 4);
-        mbar_init(&bar->pv_done[w], 1);
-        mbar_init(&bar->o_free[w], 4);
-        mbar_init(&bar->group[w], 4);
+      __syncwarp();
+      C::plan(p.w, bar->plan);
+      __syncwarp();
+      // The loads need nothing of the other warps: they start here.
+      __threadfence_block();
+      asm volatile("barrier.cta.arrive 1, 384;" ::: "memory");
+      if (bar->plan.begin < bar->plan.end) {
+        unsigned left;
+        const Piece x = C::first_piece(p.w, bar->plan, left);
+        run_loads<HD>(&q_map, &k_map, &v_map, p, smem, bar, x, left);
       }
-      mbar_init(&bar->stat_full, 4);
-      mbar_init(&bar->stat_free, 4);
-      bar->abort = 0;
-      fence_barrier_init();
-    }
-    __syncwarp();
-    C::plan(p.w, bar->plan);
-    __syncwarp();
-    // The loads need nothing of the other warps: they start here.
-    __threadfence_block();
-    asm volatile("barrier.cta.arrive 1, 384;" ::: "memory");
-    if (bar->plan.begin < bar->plan.end) {
-      unsigned left;
-      const Piece x = C::first_piece(p.w, bar->plan, left);
-      run_loads<HD>(&q_map, &k_map, &v_map, p, smem, bar, x, left);
-    }
-  } else if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == 1) {
-      tc::tmem_alloc(&bar->tmem_base, kTmemCols);
-      tc::tmem_relinquish();
-    } else if (tid == 64) {
-      tc::prefetch_tensormap(&q_map);
-      tc::prefetch_tensormap(&k_map);
-      tc::prefetch_tensormap(&v_map);
-    }
-    tc::fence_before_sync();
-    asm volatile("barrier.cta.sync 1, 384;" ::: "memory");
-    tc::fence_after_sync();
-    if (warp == 1 && bar->plan.begin < bar->plan.end) {
-      unsigned left;
-      const Piece x = C::first_piece(p.w, bar->plan, left);
-      run_products<HD>(p, smem_u32(smem), bar->tmem_base, bar, x, left);
+    } else {
+      if (warp == 1) {
+        tc::tmem_alloc(&bar->tmem_base, kTmemCols);
+        tc::tmem_relinquish();
+      } else if (tid == 64) {
+        tc::prefetch_tensormap(&q_map);
+        tc::prefetch_tensormap(&k_map);
+        tc::prefetch_tensormap(&v_map);
+      }
+      tc::fence_before_sync();
+      asm volatile("barrier.cta.sync 1, 384;" ::: "memory");
+      tc::fence_after_sync();
+      if (warp == 1 && bar->plan.begin < bar->plan.end) {
+        unsigned left;
+        const Piece x = C::first_piece(p.w, bar->plan, left);
+        run_products<HD>(p, smem_u32(smem), bar->tmem_base, bar, x, left);
+      }
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
