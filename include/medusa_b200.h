@@ -521,8 +521,8 @@ typedef struct medusa_paged_kv {
  * sets MEDUSA_ERR_DEVICE_CHECK and leaves that sequence's rows unwritten, as
  * does a page id outside [0, n_pages) for the rows in that page (where
  * attention reads such a page, its keys and values count as zeros).
- * chunk_starts that descend set it too, and attention then computes nothing;
- * so does attention over more than 2^30 blocks of keys in one call.
+ * chunk_starts that descend set it too, and the call then writes nothing; so
+ * does attention over more than 2^30 blocks of keys in one call.
  * 1 <= N <= 2^22, 1 <= H <= 256. */
 
 typedef enum medusa_rope_layout {

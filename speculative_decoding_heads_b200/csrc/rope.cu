@@ -129,14 +129,17 @@ template <typename T>
 __device__ int prepare_tokens(const RopeArgs& a, int n0, Place* place, float2* cs) {
   __shared__ int32_t starts[MEDUSA_MAX_B + 1];
   const int tid = threadIdx.x, B = a.kv.B;
+  bool none = false;
   if (a.starts) {
     for (int i = tid; i <= B; i += kThreads) starts[i] = a.starts[i];
     __syncthreads();
     if (blockIdx.x == 0 && tid < B && (starts[tid] < 0 || starts[tid + 1] < starts[tid] || starts[tid + 1] > a.N))
       set_device_status(a.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
+    // Chunks that overlap have no one owner of a row: nothing is written, as attention then computes nothing.
+    none = __syncthreads_or(tid < B && starts[tid + 1] < starts[tid]) != 0;
   }
   const int count = min(a.tok, a.N - n0);
-  if (tid < count) place[tid] = place_token(a, n0 + tid, a.starts ? starts : nullptr);
+  if (tid < count) place[tid] = none ? Place{-1, 0} : place_token(a, n0 + tid, a.starts ? starts : nullptr);
   __syncthreads();
   const int pairs = a.rot >> 1;
   for (int x = tid; x < count * pairs; x += kThreads) {

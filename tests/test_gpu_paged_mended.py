@@ -1,0 +1,41 @@
+"""The paged-cache calls on the GPU where arguments or the machine let them down."""
+
+import pytest
+import torch
+
+from test_gpu_paged import Cache, ints
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mb(built):
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import speculative_decoding_heads_b200 as mb
+    return mb
+
+
+@pytest.fixture(autouse=True)
+def no_device_error(mb):
+    mb.device_status()
+    yield
+    assert mb.device_status() == (0, 0)
+
+
+@pytest.mark.parametrize("starts", [[0, 10, 5, 12], [0, 12, 12, 11], [3, 2, 7, 12], [12, 8, 4, 0]], ids=str)
+@pytest.mark.parametrize("dtype,hd,rot", [("bf16", 128, 128), ("f32", 64, 6)], ids=["vectors", "elements"])
+def test_rope_append_writes_nothing_for_chunks_that_descend(mb, dtype, hd, rot, starts):
+    """Overlapping chunks: a row would belong to two sequences, and one of them would be left with a hole."""
+    c = Cache(mb, dtype, hd, 16, 2, [20, 10, 0], [12, 12, 12])
+    q, k = c.randn(12, 4, hd).to(c.k.dtype).cuda(), c.randn(12, 2, hd).to(c.k.dtype).cuda()
+    out = torch.full_like(q, 7.0)
+    before = c.k.clone(), c.v.clone()
+    rotary = mb.Rotary(rot)
+    mb.medusa_rope_append(c.kv, 0, q, k, k, out, rotary, chunk_starts=ints(starts))
+    assert mb.device_status() == (mb.MEDUSA_ERR_DEVICE_CHECK, 11)
+    assert (out == 7).all()
+    for now, was in zip((c.k, c.v), before):
+        assert torch.equal(now.view(torch.uint8), was.view(torch.uint8))
+    mb.medusa_rope_append(c.kv, 0, q, k, k, out, rotary, chunk_starts=ints([0, 5, 5, 12]))     # one that does not, empty chunk and all
+    assert not (out == 7).any() and not torch.equal(c.k.view(torch.uint8), before[0].view(torch.uint8))
