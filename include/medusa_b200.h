@@ -124,6 +124,17 @@ medusa_status_t medusa_device_status(int32_t* status, int32_t* detail, int clear
  * The pages have no counterpart. */
 medusa_status_t medusa_test_heads_wait(int extra_arrivals, long long limit_ns);
 
+/* The same for the two tensor-core kernels of medusa_paged_attention (bf16,
+ * head sizes 64 and 128): a barrier between two roles of a block expects
+ * extra_arrivals more than it gets, and every wait gives up after limit_ns
+ * (0: the default of about 2 s).  The status is MEDUSA_ERR_TIMEOUT, detail 14;
+ * the block's other roles stop as soon as they see it, copies and products in
+ * flight end, tensor memory is freed, and rows whose block gave up are not
+ * written.  Zero the workspace before the next call.
+ * medusa_test_paged_wait(0, 0) restores the defaults.  Process-wide.
+ * Errors: INVALID_ARG unless 0 <= extra_arrivals <= 1024 and limit_ns >= 0. */
+medusa_status_t medusa_test_paged_wait(int extra_arrivals, long long limit_ns);
+
 /* ------------------------------------------------------------------------ */
 /* Candidate tree                                                            */
 /* ------------------------------------------------------------------------ */

@@ -24,8 +24,9 @@ enum DeviceDetail : int {
   kDetailPagedChunk = 11,     // paged calls: a chunk outside the packed rows, or a sequence past its page table
   kDetailPagedPage = 12,      // paged calls: a page id outside [0, n_pages)
   kDetailPagedAccept = 13,    // paged_accept_kv: bad path, accept length or sequence length
-  kDetailPagedWait = 14,      // paged attention: a copy or product never completed
+  kDetailPagedWait = 14,      // paged attention: a wait for a copy, a product or another role of the block ran out
   kDetailLogitHistory = 15,   // adjust_logits: a history length outside its buffer
+  kDetailPagedShared = 16,    // paged attention: dynamic shared memory not on a 1024-byte boundary
 };
 
 // Address of the current device's status word ([0] status, [1] detail).
@@ -103,13 +104,13 @@ __device__ __forceinline__ void mbar_arrive_cta(uint64_t* bar) {
 }
 
 // Waits for the phase with the given parity to complete; gives up after
-// kSpinLimitNs and returns false.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity) {
+// limit_ns and returns false.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, uint64_t limit_ns = kSpinLimitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = globaltimer_ns();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try_wait(bar, parity)) return true;
-    if ((it & 255u) == 0 && globaltimer_ns() - t0 > kSpinLimitNs) return false;
+    if ((it & 255u) == 0 && globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
 

@@ -175,6 +175,12 @@ size_t paged_attention_workspace_bytes(const PagedDev& kv, medusa_dtype_t dtype,
 medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype, int N, int H, const void* q,
                                        float scale, const TreeDev* tree, const int32_t* starts, void* out, void* ws,
                                        cudaStream_t stream);
+// What medusa_test_paged_wait asks of later launches (paged_api.cu).
+struct PagedWait {
+  unsigned extra;
+  unsigned long long limit_ns;
+};
+PagedWait paged_wait();
 // Its tensor-core kernel (paged_attention_tc.cu): bf16, hd 64 or 128.
 bool paged_attention_tc_supported(const PagedDev& kv, medusa_dtype_t dtype, int H);
 size_t paged_attention_tc_workspace_bytes(const PagedDev& kv, int N, int H);

@@ -1,5 +1,6 @@
 // The C ABI of the paged-cache calls and of the logit adjustment: argument
 // checks on the host before any launch, and the table of rotary frequencies.
+#include <atomic>
 #include <cmath>
 #include <string>
 
@@ -70,10 +71,27 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return x < y + bn && y < x + an;
 }
 
+std::atomic<unsigned> g_test_extra{0};
+std::atomic<unsigned long long> g_test_limit_ns{0};
+
 }  // namespace
+
+PagedWait paged_wait() {
+  const unsigned long long lim = g_test_limit_ns.load();
+  return {g_test_extra.load(), lim ? lim : kSpinLimitNs};
+}
+
 }  // namespace medusa
 
 using namespace medusa;
+
+extern "C" medusa_status_t medusa_test_paged_wait(int extra_arrivals, long long limit_ns) {
+  if (extra_arrivals < 0 || extra_arrivals > 1024 || limit_ns < 0)
+    return fail(MEDUSA_ERR_INVALID_ARG, "medusa_test_paged_wait: extra_arrivals in [0, 1024], limit_ns >= 0");
+  g_test_extra.store(static_cast<unsigned>(extra_arrivals));
+  g_test_limit_ns.store(static_cast<unsigned long long>(limit_ns));
+  return MEDUSA_OK;
+}
 
 extern "C" medusa_status_t medusa_rotary_turns(int rot, double base, medusa_rope_scaling_t scaling, double factor,
                                                int original_length, double beta_fast, double beta_slow,

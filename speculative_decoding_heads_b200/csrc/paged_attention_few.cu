@@ -69,11 +69,11 @@ struct Params {
 };
 
 // A whole warp waits and agrees on the outcome.
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, int* status) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, const Work& w) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const bool ok = *reinterpret_cast<volatile int*>(&b->abort) == 0 && mbar_wait(bar, parity);
+  const bool ok = *reinterpret_cast<volatile int*>(&b->abort) == 0 && mbar_wait(bar, parity, w.wait_limit);
   if (__all_sync(0xffffffffu, ok)) return true;
-  set_device_status(status, MEDUSA_ERR_TIMEOUT, kDetailPagedWait);
+  set_device_status(w.status, MEDUSA_ERR_TIMEOUT, kDetailPagedWait);
   *reinterpret_cast<volatile int*>(&b->abort) = 1;
   return false;
 }
@@ -120,7 +120,7 @@ __device__ void run_loads(const CUtensorMap* k_map, const CUtensorMap* v_map, co
   };
   auto entry = [&](const CUtensorMap* map, int kb, int block) {
     const int st = e % S::kStages;
-    if (e >= S::kStages && !wait(&bar->empty[st], (e / S::kStages - 1) & 1, bar, p.w.status)) return false;
+    if (e >= S::kStages && !wait(&bar->empty[st], (e / S::kStages - 1) & 1, bar, p.w)) return false;
     unsigned char* d = smem + st * S::kTile;
     if (lane == 0) mbar_arrive_expect_tx(&bar->full[st], S::kTile);
     __syncwarp();
@@ -145,7 +145,7 @@ __device__ void run_loads(const CUtensorMap* k_map, const CUtensorMap* v_map, co
   }
   // Every copy issued lands before the CTA exits (bounded).
   for (int st = 0; st < S::kStages; ++st)
-    if (e > st) mbar_wait(&bar->full[st], ((e - 1 - st) / S::kStages) & 1);
+    if (e > st) mbar_wait(&bar->full[st], ((e - 1 - st) / S::kStages) & 1, p.w.wait_limit);
 }
 
 // ---- the eight computing warps ------------------------------------------------
@@ -158,7 +158,6 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, gr = lane >> 2, qc = lane & 3;
   const Plan& pl = bar->plan;
   const int g = p.w.g;
-  int* status = p.w.status;
   const uint32_t ring = smem_u32(smem);
   float* join = reinterpret_cast<float*>(smem + S::kOffJoin);
   int st = 0, ph = 0, syncs = 0;
@@ -171,7 +170,7 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
   auto all = [&] {                                     // the computing warps
     __syncwarp();
     if (lane == 0) mbar_arrive_cta(&bar->group);
-    return wait(&bar->group, syncs++ & 1, bar, status);
+    return wait(&bar->group, syncs++ & 1, bar, p.w);
   };
   // ldmatrix rows: K (keys x dimensions) and V (transposed) of this warp's 16 keys.
   const int k_key = 16 * warp + (lane >> 4) * 8 + (lane & 7), k_ch = (lane >> 3) & 1;
@@ -213,7 +212,7 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
       for (int e = 0; e < 4; ++e) o[c][e] = 0.f;
     for (int kb = x.kb0; kb < x.kb1; ++kb) {
       const int j0 = kb * kBK, mine = keys - j0 - 16 * warp;    // keys of this warp's 16
-      if (!wait(&bar->full[st], ph, bar, status)) return;
+      if (!wait(&bar->full[st], ph, bar, p.w)) return;
       const uint32_t kt = ring + st * S::kTile;
       float s[2][4];
       if (mine > 0) {
@@ -290,7 +289,7 @@ __device__ void run_rows(const Params& p, unsigned char* smem, Bars* bar, Piece 
             pl_[2 * u + i] = pack2(a - bf16lo(h), d - bf16hi(h));
           }
       }
-      if (!wait(&bar->full[st], ph, bar, status)) return;
+      if (!wait(&bar->full[st], ph, bar, p.w)) return;
       const uint32_t vt = ring + st * S::kTile;
       if (mine > 0) {
         const bool stale = mine < 16;                  // rows past the sequence may hold anything: 0 * value must stay 0
@@ -485,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<HD>;
   extern __shared__ __align__(1024) unsigned char smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {      // the swizzle pattern needs it; no static shared memory precedes it
-    if (threadIdx.x == 0) set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedWait);
+    if (threadIdx.x == 0) set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedShared);
     return;
   }
   Bars* bar = reinterpret_cast<Bars*>(smem + S::kOffBars);
@@ -496,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(&bar->full[st], 1);
         mbar_init(&bar->empty[st], kWarps);
       }
-      mbar_init(&bar->group, kWarps);
+      mbar_init(&bar->group, kWarps + p.w.wait_extra);
       bar->abort = 0;
       fence_barrier_init();
     }
@@ -544,6 +543,8 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.extra = 4u;          // 11 ragged tokens of 32 heads up to 12308 rows 32.5 us (0: 39), 29 of 40 heads 105 (0: 117, 6: 113)
   p.w.starts = starts;
   p.w.status = device_status_ptr();
+  p.w.wait_limit = paged_wait().limit_ns;
+  p.w.wait_extra = paged_wait().extra;
   const int page = 1 << kv.page_shift;
   p.box = page < kBK ? page : kBK;
   p.q = static_cast<const uint16_t*>(q);

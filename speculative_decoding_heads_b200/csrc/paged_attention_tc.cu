@@ -69,6 +69,7 @@ struct Bars {
   uint64_t full[8], empty[8];
   uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2], p_half[2], p_full[2], pv_done[2], o_free[2];
+  uint64_t drain;
   uint64_t stat_full, stat_free, group[2];   // statistics handed over; the warps of one warpgroup
   uint32_t tmem_base;
   int abort, last[2];
@@ -93,11 +94,11 @@ struct Params {
 
 // A whole warp waits and agrees on the outcome (a wait that runs out in one
 // lane ends the role for all of them).
-__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, int* status) {
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, Bars* b, const Work& w) {
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-  const bool ok = *reinterpret_cast<volatile int*>(&b->abort) == 0 && mbar_wait(bar, parity);
+  const bool ok = *reinterpret_cast<volatile int*>(&b->abort) == 0 && mbar_wait(bar, parity, w.wait_limit);
   if (__all_sync(0xffffffffu, ok)) return true;
-  set_device_status(status, MEDUSA_ERR_TIMEOUT, kDetailPagedWait);
+  set_device_status(w.status, MEDUSA_ERR_TIMEOUT, kDetailPagedWait);
   *reinterpret_cast<volatile int*>(&b->abort) = 1;
   return false;
 }
@@ -172,7 +173,7 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
   };
   auto entry = [&](const CUtensorMap* map, int kb, int block) {
     const int st = e % S::kStages;
-    if (e >= S::kStages && !wait(&bar->empty[st], (e / S::kStages - 1) & 1, bar, p.w.status)) return false;
+    if (e >= S::kStages && !wait(&bar->empty[st], (e / S::kStages - 1) & 1, bar, p.w)) return false;
     unsigned char* d = smem + S::kOffRing + st * S::kTile;
     if (lane == 0) mbar_arrive_expect_tx(&bar->full[st], S::kTile);
     __syncwarp();
@@ -186,7 +187,7 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
     return true;
   };
   auto query = [&](int w, int b, int h, int row0) {
-    if (nq[w] > 0 && !wait(&bar->q_empty[w], (nq[w] - 1) & 1, bar, p.w.status)) return false;
+    if (nq[w] > 0 && !wait(&bar->q_empty[w], (nq[w] - 1) & 1, bar, p.w)) return false;
     if (lane == 0) {
       mbar_arrive_expect_tx(&bar->q_full[w], S::kHalves * p.w.g * p.q_tokens * 128);
       for (int hf = 0; hf < S::kHalves; ++hf)
@@ -218,9 +219,9 @@ __device__ void run_loads(const CUtensorMap* q_map, const CUtensorMap* k_map, co
   }
   // Every copy issued lands before the CTA exits (bounded).
   for (int st = 0; st < S::kStages; ++st)
-    if (e > st) mbar_wait(&bar->full[st], ((e - 1 - st) / S::kStages) & 1);
+    if (e > st) mbar_wait(&bar->full[st], ((e - 1 - st) / S::kStages) & 1, p.w.wait_limit);
   for (int w = 0; w < 2; ++w)
-    if (nq[w] > 0) mbar_wait(&bar->q_full[w], (nq[w] - 1) & 1);
+    if (nq[w] > 0) mbar_wait(&bar->q_full[w], (nq[w] - 1) & 1, p.w.wait_limit);
 }
 
 // ---- products (warp 1) -------------------------------------------------------
@@ -240,7 +241,6 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
   constexpr uint32_t idS = tc::idesc_bf16_f32(kGroup, kBK, 0);
   constexpr uint32_t idO = tc::idesc_bf16_f32(kGroup, HD, 1);
   const Plan& pl = bar->plan;
-  int* status = p.w.status;
   int st = 0, ph = 0;                        // the next ring entry's stage and parity
   int nq[2] = {0, 0}, np[2] = {0, 0}, piece = 0;
   const uint32_t ring = sbase + S::kOffRing;
@@ -253,7 +253,7 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
       ph ^= 1;
     }
   };
-  auto landed = [&] { return wait(&bar->full[st], ph, bar, status); };
+  auto landed = [&] { return wait(&bar->full[st], ph, bar, p.w); };
   auto scores = [&](int w, int q, bool release, bool last) {          // S_w = Q_q K^T
     const uint64_t qd = q0 + q * (S::kTile >> 4), kd = k0 + static_cast<uint64_t>(st) * (S::kTile >> 4);
     tc::fence_after_sync();
@@ -274,8 +274,8 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
     const uint64_t vd = v0 + static_cast<uint64_t>(st) * (S::kTile >> 4);
     const uint32_t o = tmem + 256 + 128 * w, ps = tmem + 128 * w;
     if (!landed()) return false;
-    if (first && piece > 0 && !wait(&bar->o_free[w], (piece - 1) & 1, bar, status)) return false;
-    if (!wait(&bar->p_half[w], np[w] & 1, bar, status)) return false;
+    if (first && piece > 0 && !wait(&bar->o_free[w], (piece - 1) & 1, bar, p.w)) return false;
+    if (!wait(&bar->p_half[w], np[w] & 1, bar, p.w)) return false;
     tc::fence_after_sync();
     if (elect_one()) {
 #pragma unroll
@@ -283,7 +283,7 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
         if (c < 2 * chunks) tc::mma_ts(o, ps + c * 8, vd + c * (16 * 128 >> 4), idO, (!first || c > 0) ? 1u : 0u);
     }
     __syncwarp();
-    if (!wait(&bar->p_full[w], np[w] & 1, bar, status)) return false;
+    if (!wait(&bar->p_full[w], np[w] & 1, bar, p.w)) return false;
     ++np[w];
     tc::fence_after_sync();
     if (elect_one()) {
@@ -299,12 +299,12 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
   for (;;) {
     const Seg s = segment(p, pl, x);
     const int keys = C::keys(p.w, pl, x.b, x.tile);
-    if (!wait(&bar->q_full[0], nq[0] & 1, bar, status)) return;
+    if (!wait(&bar->q_full[0], nq[0] & 1, bar, p.w)) return;
     ++nq[0];
     if (s.two) {
       if (!landed()) return;
       scores(0, 0, false, s.n == 1);
-      if (!wait(&bar->q_full[1], nq[1] & 1, bar, status)) return;
+      if (!wait(&bar->q_full[1], nq[1] & 1, bar, p.w)) return;
       ++nq[1];
       scores(1, 1, true, s.n == 1);
       next();
@@ -334,7 +334,7 @@ __device__ void run_products(const Params& p, uint32_t sbase, uint32_t tmem, Bar
         next();
       }
       // No phase of a barrier goes by unseen, where the first warpgroup has no tile either.
-      if (s.n == 1 && piece > 0 && !wait(&bar->o_free[0], (piece - 1) & 1, bar, status)) return;
+      if (s.n == 1 && piece > 0 && !wait(&bar->o_free[0], (piece - 1) & 1, bar, p.w)) return;
       for (int i = 0; i < s.n; ++i) {
         if (!values(1 - (i & 1), i < 2, tile_chunks(keys - (x.kb0 + i) * kBK), true)) return;
         next();
@@ -464,7 +464,6 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
   const uint32_t lanes = static_cast<uint32_t>(32 * quarter) << 16;
   const uint32_t tS = tmem + lanes + 128 * w;
   const Plan& pl = bar->plan;
-  int* status = p.w.status;
   int steps = 0;                             // tiles this warpgroup has taken
   int pv[2] = {0, 0};                        // P V products of both warpgroups before this piece
   int entries = 0;                           // ring entries before this piece
@@ -511,7 +510,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           for (int c = 0; c < 4; ++c) bits[c] = static_cast<uint32_t>(tree_bits(anc, L - j0 - 32 * c));
         }
       }
-      if (!wait(&bar->s_full[w], steps & 1, bar, status)) return;
+      if (!wait(&bar->s_full[w], steps & 1, bar, p.w)) return;
       tc::fence_after_sync();
       const bool zero = (w == 0 || !s.two) && x.kb0 + i == x.blocks - 1 && (keys & (p.box - 1)) != 0;
       if (active) {
@@ -576,7 +575,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
         // Rows of the last page past the sequence may hold anything: zero
         // their values, so that 0 * (stale value) stays 0.
         const int v = entries + 2 * s.n - 1;            // a piece's last ring entry
-        if (!wait(&bar->full[v % S::kStages], (v / S::kStages) & 1, bar, status)) return;
+        if (!wait(&bar->full[v % S::kStages], (v / S::kStages) & 1, bar, p.w)) return;
         const int r0 = keys - j0, r1 = (r0 + p.box - 1) & ~(p.box - 1);
         unsigned char* d = smem + S::kOffRing + (v % S::kStages) * S::kTile + r0 * 128;
         for (int c = row; c < (r1 - r0) * 8; c += kGroup)
@@ -597,12 +596,12 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
     if (!s.two) {
       if (w == 1) {
         // the first warpgroup has read the last hand-over
-        if (singles > 0 && !wait(&bar->stat_free, (singles - 1) & 1, bar, status)) return;
+        if (singles > 0 && !wait(&bar->stat_free, (singles - 1) & 1, bar, p.w)) return;
         bar->m1[row] = m;
         bar->l1[row] = l;
         arrive(&bar->stat_full);
       } else {
-        if (!wait(&bar->stat_full, singles & 1, bar, status)) return;
+        if (!wait(&bar->stat_full, singles & 1, bar, p.w)) return;
         const float m1 = bar->m1[row], l1 = bar->l1[row], mm = fmaxf(m, m1);
         arrive(&bar->stat_free);
         f0 = m == -INFINITY ? 0.f : tc::ex2_ftz(m - mm);
@@ -615,8 +614,8 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
     }
     if (s.two || w == 0) {
       const int own = s.two ? w : 1;           // the first tile of an alternating unit is the second warpgroup's
-      if (second && !wait(&bar->pv_done[0], (pv[0] + n0 - 1) & 1, bar, status)) return;
-      if (!wait(&bar->pv_done[own], (pv[own] + (own == 0 ? n0 : n1) - 1) & 1, bar, status)) return;
+      if (second && !wait(&bar->pv_done[0], (pv[0] + n0 - 1) & 1, bar, p.w)) return;
+      if (!wait(&bar->pv_done[own], (pv[own] + (own == 0 ? n0 : n1) - 1) & 1, bar, p.w)) return;
       tc::fence_after_sync();
       const bool whole = C::whole(x);
       const int slot_row = (s.two ? w * kGroup : 0) + row;           // rows of a slot: 2 * kGroup
@@ -668,7 +667,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           __stcg(slot + 2 * kGroup + slot_row, l);
         }
         arrive(&bar->group[w]);                // then one thread's release covers all of them
-        if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
+        if (!wait(&bar->group[w], syncs++ & 1, bar, p.w)) return;
         int lo, hi;
         C::owners(pl, x, lo, hi);
         if (row == 0) {
@@ -677,7 +676,7 @@ __device__ void run_softmax(const Params& p, unsigned char* smem, uint32_t tmem,
           if (bar->last[w]) *ctr = 0u;
         }
         arrive(&bar->group[w]);
-        if (!wait(&bar->group[w], syncs++ & 1, bar, status)) return;
+        if (!wait(&bar->group[w], syncs++ & 1, bar, p.w)) return;
         if (bar->last[w]) {
           const int row0 = s.two ? w * kGroup : 0;
           // Few rows or many pieces: more pieces at a time; else more rows.
@@ -700,7 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   using S = Shape<HD>;
   extern __shared__ __align__(1024) unsigned char smem[];
   if ((smem_u32(smem) & 1023u) != 0u) {      // the swizzle pattern needs it; no static shared memory precedes it
-    if (threadIdx.x == 0) set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedWait);
+    if (threadIdx.x == 0) set_device_status(p.w.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedShared);
     return;
   }
   Bars* bar = reinterpret_cast<Bars*>(smem + S::kOffBars);
@@ -720,12 +719,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_init(&bar->q_full[w], 1);
           mbar_init(&bar->q_empty[w], 1);
           mbar_init(&bar->s_full[w], 1);
-          mbar_init(&bar->p_half[w], 4);
+          mbar_init(&bar->p_half[w], 4 + p.w.wait_extra);
           mbar_init(&bar->p_full[w], 4);
           mbar_init(&bar->pv_done[w], 1);
           mbar_init(&bar->o_free[w], 4);
           mbar_init(&bar->group[w], 4);
         }
+        mbar_init(&bar->drain, 1);
         mbar_init(&bar->stat_full, 4);
         mbar_init(&bar->stat_free, 4);
         bar->abort = 0;
@@ -758,6 +758,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned left;
         const Piece x = C::first_piece(p.w, bar->plan, left);
         run_products<HD>(p, smem_u32(smem), bar->tmem_base, bar, x, left);
+        // However it ended: products in flight end before their operands and tensor memory go (bounded).
+        if (elect_one()) tc::mma_commit(&bar->drain);
+        __syncwarp();
+        mbar_wait(&bar->drain, 0, p.w.wait_limit);
       }
     }
   } else {
@@ -802,6 +806,8 @@ medusa_status_t launch(const PagedDev& kv, int N, int H, const void* q, float sc
   p.w.g = H / kv.Hkv;
   p.w.starts = starts;
   p.w.status = device_status_ptr();
+  p.w.wait_limit = paged_wait().limit_ns;
+  p.w.wait_extra = paged_wait().extra;
   const int tokens = kGroup / p.w.g;
   p.rows = tokens * p.w.g;
   p.w.R = rows_per_unit(N, H, p.rows);

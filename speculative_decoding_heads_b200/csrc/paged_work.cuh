@@ -66,6 +66,8 @@ struct Work {
   float* slots;            // 2 per CTA, at the start of the workspace
   unsigned* counters;      // kCounters per unit, zero between calls
   int* status;
+  uint64_t wait_limit;     // ns after which a wait gives up
+  unsigned wait_extra;     // test hook: arrivals that one barrier expects and never gets
 };
 
 struct Plan {

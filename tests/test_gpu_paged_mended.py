@@ -39,3 +39,39 @@ def test_rope_append_writes_nothing_for_chunks_that_descend(mb, dtype, hd, rot, 
         assert torch.equal(now.view(torch.uint8), was.view(torch.uint8))
     mb.medusa_rope_append(c.kv, 0, q, k, k, out, rotary, chunk_starts=ints([0, 5, 5, 12]))     # one that does not, empty chunk and all
     assert not (out == 7).any() and not torch.equal(c.k.view(torch.uint8), before[0].view(torch.uint8))
+
+
+WAITS = {  # hd, page, H, Hkv, lens, news
+    "few rows": (128, 16, 8, 2, [300, 1500, 40], [1, 1, 1]),
+    "alternating tiles": (64, 16, 8, 2, [300, 90], [40, 11]),
+    "two groups of rows": (128, 64, 64, 8, [300, 40], [500, 140]),
+}
+
+
+@pytest.mark.parametrize("case", sorted(WAITS))
+def test_a_wait_that_runs_out_ends_the_call(mb, case):
+    """A barrier between two roles expects one arrival that nobody makes, for at most 1 ms: the call reports it, writes
+    none of the rows (no piece is finished), and leaves a context in which the next call, its workspace zeroed, is exact."""
+    hd, page, H, Hkv, lens, news = WAITS[case]
+    c = Cache(mb, "bf16", hd, page, Hkv, lens, news)
+    N, starts = sum(news), ints([sum(news[:b]) for b in range(len(news) + 1)])
+    q = c.randn(N, H, hd).bfloat16().cuda()
+    ws = mb.workspace(mb.medusa_paged_attention_workspace_size(c.kv, N, H))
+    want, out = torch.empty_like(q), torch.full_like(q, 7.0)
+    args = dict(chunk_starts=None if case == "few rows" else starts)
+    mb.medusa_paged_attention(c.kv, 0, q, want, hd ** -0.5, ws, **args)
+    torch.cuda.synchronize()
+    assert mb.device_status() == (0, 0)
+    try:
+        mb.medusa_test_paged_wait(1, 1_000_000)
+        mb.medusa_paged_attention(c.kv, 0, q, out, hd ** -0.5, ws, **args)
+        torch.cuda.synchronize()
+    finally:
+        mb.medusa_test_paged_wait(0, 0)
+    assert mb.device_status() == (mb.MEDUSA_ERR_TIMEOUT, 14)
+    assert (out == 7).all()
+    ws.zero_()
+    for _ in range(2):
+        mb.medusa_paged_attention(c.kv, 0, q, out, hd ** -0.5, ws, **args)
+        assert torch.equal(out, want)
+        out.fill_(7.0)
