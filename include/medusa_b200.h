@@ -507,7 +507,8 @@ medusa_status_t medusa_generate_greedy(const medusa_tree_t* tree, const medusa_d
  *              hold rows of the sequence (new tokens included) are read
  *   seq_lens   [B] int32 device
  * dtype MEDUSA_F32 or MEDUSA_BF16; page a power of two in [8, 256]; hd a
- * multiple of 8 in [8, 256]; 1 <= B <= MEDUSA_MAX_B.  Rows of a page past the
+ * multiple of 8 in [8, 256]; 1 <= B <= MEDUSA_MAX_B.  A sequence has at most
+ * 2^31 - 257 rows, however wide its table.  Rows of a page past the
  * sequence's last row may hold anything.  A page that several sequences share
  * (a common prefix) may be read by all of them; the rows that a call writes
  * must belong to one sequence.  The struct holds pointers only; the calls do
@@ -528,8 +529,9 @@ typedef struct medusa_paged_kv {
  * ascending from 0, last entry <= N; rows behind it are left as they were),
  * or, with chunk_starts NULL, N / B rows each (N a multiple of B).  Token i of
  * sequence b is cache row seq_lens[b] + i.  A chunk may be empty.  A chunk
- * outside [0, N), a negative length, or seq_lens[b] + chunk > max_pages * page
- * sets MEDUSA_ERR_DEVICE_CHECK and leaves that sequence's rows unwritten, as
+ * outside [0, N), a negative length, or a sequence that would outgrow its table
+ * or 2^31 - 257 rows sets MEDUSA_ERR_DEVICE_CHECK and leaves that sequence's
+ * rows unwritten, as
  * does a page id outside [0, n_pages) for the rows in that page (where
  * attention reads such a page, its keys and values count as zeros).
  * chunk_starts that descend set it too, and the call then writes nothing; so

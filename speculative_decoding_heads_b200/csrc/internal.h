@@ -158,6 +158,10 @@ medusa_status_t launch_tree_decode(const TreeDev& t, const medusa_decoder_t* m, 
                                    void* k_cache, void* v_cache, int Lcap, const int32_t* seq_lens,
                                    float* logits, float* hidden, void* ws, cudaStream_t stream);
 
+// Rows that a sequence of the paged cache may have, new ones included: their
+// numbers, rounded up to a block of keys, stay inside 31 bits.
+constexpr long long kMaxPagedRows = 0x7ffffeff;
+
 // The paged cache as kernels see it (paged_api.cu builds it from checked arguments).
 struct PagedDev {
   int n_pages, Hkv, page_shift, hd, B, max_pages;

@@ -37,7 +37,7 @@ __device__ __forceinline__ int accepted(const AcceptArgs& a, int b, int* L, int*
   *L = a.kv.lens[b];
   *best = a.best_path[b];
   const int n = a.accept_len[b];
-  const long long cap = static_cast<long long>(a.kv.max_pages) << a.kv.page_shift;
+  const long long cap = min(static_cast<long long>(a.kv.max_pages) << a.kv.page_shift, kMaxPagedRows);
   if (*L < 0 || n < 0 || n > a.t.D || *best < 0 || *best >= a.t.P || static_cast<long long>(*L) + a.t.T > cap) return -1;
   return a.t.retrieve[*best * (a.t.D + 1) + n] < 0 ? -1 : n;
 }

@@ -37,7 +37,7 @@ medusa_status_t check_kv(const medusa_paged_kv_t* kv, const char* fn) {
 
 int element_bytes(medusa_dtype_t t) { return t == MEDUSA_BF16 ? 2 : 4; }
 
-// Sequences hold at most 2^31 - 1 rows; a longer table's tail is never used.
+// Sequences hold at most kMaxPagedRows rows; a longer table's tail is never used.
 PagedDev device_view(const medusa_paged_kv_t* kv, int layer) {
   PagedDev d{};
   d.n_pages = kv->n_pages;

@@ -162,7 +162,7 @@ struct Cut {
         }
         const bool ok = n[i] == 0 || (n[i] > 0 && first[i] >= 0 && first[i] <= w.N - n[i] && L[i] >= 0 &&
                                       static_cast<long long>(L[i]) + n[i] <= cap &&
-                                      static_cast<long long>(L[i]) + n[i] < 0x7fffff00ll);
+                                      static_cast<long long>(L[i]) + n[i] <= kMaxPagedRows);
         if (!ok) {
           n[i] = 0;
           bad = true;

@@ -64,7 +64,7 @@ __device__ Place place_token(const RopeArgs& a, int n, const int32_t* starts /* 
     if (first < 0 || n < first || n >= last || last > a.N) return pl;   // behind the last sequence, or no chunk
   }
   const int L = a.kv.lens[b];
-  const long long cap = static_cast<long long>(a.kv.max_pages) << a.kv.page_shift;
+  const long long cap = min(static_cast<long long>(a.kv.max_pages) << a.kv.page_shift, kMaxPagedRows);
   if (L < 0 || static_cast<long long>(L) + (last - first) > cap) {
     set_device_status(a.status, MEDUSA_ERR_DEVICE_CHECK, kDetailPagedChunk);
     return pl;

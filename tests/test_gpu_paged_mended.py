@@ -3,6 +3,7 @@
 import pytest
 import torch
 
+import oracle.medusa_oracle as O
 from test_gpu_paged import Cache, ints
 
 pytestmark = pytest.mark.gpu
@@ -75,3 +76,44 @@ def test_a_wait_that_runs_out_ends_the_call(mb, case):
         mb.medusa_paged_attention(c.kv, 0, q, out, hd ** -0.5, ws, **args)
         assert torch.equal(out, want)
         out.fill_(7.0)
+
+
+MOST_ROWS = 2 ** 31 - 257
+
+
+def test_the_most_rows_of_a_sequence(mb):
+    """Row numbers stay inside 31 bits: the append, attention and the compaction refuse a sequence that would pass them,
+    as one that outgrows its table, and serve the longest that does not.  Every entry of the table is page 0, so a cache
+    of two pages stands for all of it; the first sequence is short and always served."""
+    hd, page, T = 8, 256, 7
+    pages = torch.zeros(1, 2, 1, page, hd, device="cuda")
+    table = torch.zeros(2, 2 ** 31 // page + 2, dtype=torch.int32, device="cuda")
+    table[0] = 1
+    tree = mb.Tree(O.ranksum_choices(2, 2, T - 1), 2, 2)
+    assert tree.T == T
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.randn(2 * T, 1, hd, generator=g, device="cuda")
+    rotary = mb.Rotary(hd)
+    for L, ok in ((MOST_ROWS - T, True), (MOST_ROWS - T + 1, False), (2 ** 31 - 3, False), (2 ** 31 - 1, False)):
+        kv = mb.PagedKV(pages.clone(), pages.clone(), table, ints([3, L]))
+        before = kv.v_pages.clone()
+        out = torch.full_like(x, 7.0)
+        mb.medusa_rope_append(kv, 0, x, x, x, out, rotary)
+        assert mb.device_status() == ((0, 0) if ok else (mb.MEDUSA_ERR_DEVICE_CHECK, 11))
+        assert not (out[:T] == 7).any() and (out[T:] == 7).all() == (not ok)
+        assert torch.equal(kv.v_pages[0, 1, 0, 3:3 + T], x[:T, 0])
+        assert torch.equal(kv.v_pages[0, 0], before[0, 0]) == (not ok)
+        if ok:
+            assert torch.equal(kv.v_pages[0, 0, 0, [r % page for r in range(L, L + T)]], x[T:, 0])
+        new = ints([-5, -5])
+        ws = mb.workspace(mb.medusa_paged_accept_workspace_size(kv))
+        mb.medusa_paged_accept_kv(tree, kv, ints([0, 0]), ints([1, 1]), new, ws)
+        assert mb.device_status() == ((0, 0) if ok else (mb.MEDUSA_ERR_DEVICE_CHECK, 13))
+        assert new.tolist() == [5, L + 2 if ok else -5]
+    # attention computes over such a sequence only where it is refused: 2^31 rows would take the test's time
+    kv = mb.PagedKV(pages, pages, table, ints([3, MOST_ROWS]))
+    ws = mb.workspace(mb.medusa_paged_attention_workspace_size(kv, 2, 1))
+    out = torch.full_like(x[:2], 7.0)
+    mb.medusa_paged_attention(kv, 0, x[:2].contiguous(), out, 1.0, ws)
+    assert mb.device_status() == (mb.MEDUSA_ERR_DEVICE_CHECK, 11)
+    assert out[0].isfinite().all() and not (out[0] == 7).any() and (out[1] == 7).all()
