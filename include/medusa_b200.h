@@ -575,7 +575,8 @@ typedef struct medusa_rotary {
  *              q_stride / k_stride / v_stride elements apart (heads dense; a
  *              multiple of 16 bytes), so the three may be slices of one fused
  *              product's output
- *   q_out [N, H, hd] contiguous; may be q itself when q is contiguous
+ *   q_out [N, H, hd] contiguous; may be q itself when q is contiguous; none of
+ *              q, k, v and q_out may lie in the pages
  *   positions [N] int32 device: the rotation's position of every token (the
  *              tree's position_ids), or NULL: the token's cache row
  * (x, y) -> amplitude (x cos - y sin, y cos + x sin) in fp32, rounded once to
@@ -599,7 +600,8 @@ size_t medusa_paged_attention_workspace_size(const medusa_paged_kv_t* kv, int N,
  *   tree NULL   j <= L + i: a chunk of a prompt, or one token (decoding)
  *   tree given  j < L, and L + t for t = i and its ancestors: N = B * T rows,
  *               chunk_starts must be NULL
- *   q, out [N, H, hd] contiguous in the cache's dtype, H a multiple of Hkv.
+ *   q, out [N, H, hd] contiguous in the cache's dtype, H a multiple of Hkv;
+ *              out apart from q and from the pages.
  * fp32 scores, softmax and accumulation; in bf16 the probabilities enter the
  * second product rounded to bf16 and the output is rounded once.  |scale| is
  * at most 2^64.  Results do not depend on the order in which the GPU runs the

@@ -71,6 +71,12 @@ bool overlap(const void* a, size_t an, const void* b, size_t bn) {
   return x < y + bn && y < x + an;
 }
 
+// Whether [a, a + an) holds a byte of the cache's pages.
+bool in_pages(const medusa_paged_kv_t* kv, const void* a, size_t an) {
+  const size_t bytes = static_cast<size_t>(kv->layers) * kv->n_pages * kv->Hkv * kv->page * kv->hd * element_bytes(kv->dtype);
+  return overlap(a, an, kv->k_pages, bytes) || overlap(a, an, kv->v_pages, bytes);
+}
+
 std::atomic<unsigned> g_test_extra{0};
 std::atomic<unsigned long long> g_test_limit_ns{0};
 
@@ -159,11 +165,13 @@ extern "C" medusa_status_t medusa_rope_append(const medusa_paged_kv_t* kv, int l
       !aligned(positions, 4))
     return fail(MEDUSA_ERR_INVALID_ARG, f + ": misaligned pointer");
   const size_t span_q = (static_cast<size_t>(N - 1) * q_stride + qw) * es, out_bytes = static_cast<size_t>(N) * qw * es;
+  const size_t span_k = (static_cast<size_t>(N - 1) * k_stride + kw) * es, span_v = (static_cast<size_t>(N - 1) * v_stride + kw) * es;
   if (q_out == q ? q_stride != qw : overlap(q, span_q, q_out, out_bytes))
     return fail(MEDUSA_ERR_INVALID_ARG, f + ": q_out may be q itself when q is contiguous, and must not overlap it otherwise");
-  if (overlap(k, (static_cast<size_t>(N - 1) * k_stride + kw) * es, q_out, out_bytes) ||
-      overlap(v, (static_cast<size_t>(N - 1) * v_stride + kw) * es, q_out, out_bytes))
+  if (overlap(k, span_k, q_out, out_bytes) || overlap(v, span_v, q_out, out_bytes))
     return fail(MEDUSA_ERR_INVALID_ARG, f + ": q_out overlaps k or v");
+  if (in_pages(kv, q_out, out_bytes) || in_pages(kv, q, span_q) || in_pages(kv, k, span_k) || in_pages(kv, v, span_v))
+    return fail(MEDUSA_ERR_INVALID_ARG, f + ": q, k, v or q_out overlaps the pages");
   if (sm_count() <= 0) return fail(MEDUSA_ERR_CUDA, f + ": no usable CUDA device");
   return launch_rope_append(device_view(kv, layer), kv->dtype, N, H, q, q_stride, k, k_stride, v, v_stride, q_out,
                             *rotary, positions, chunk_starts, stream);
@@ -192,6 +200,7 @@ extern "C" medusa_status_t medusa_paged_attention(const medusa_paged_kv_t* kv, i
     return fail(MEDUSA_ERR_INVALID_ARG, f + ": misaligned pointer");
   const size_t bytes = static_cast<size_t>(N) * H * kv->hd * element_bytes(kv->dtype);
   if (overlap(q, bytes, out, bytes)) return fail(MEDUSA_ERR_INVALID_ARG, f + ": out overlaps q");
+  if (in_pages(kv, out, bytes)) return fail(MEDUSA_ERR_INVALID_ARG, f + ": out overlaps the pages");
   if (tree) {
     st = check_tree(tree, fn);
     if (st != MEDUSA_OK) return st;
