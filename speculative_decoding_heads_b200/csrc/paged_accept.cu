@@ -23,7 +23,7 @@ constexpr int kMaxRows = MEDUSA_MAX_K + 1;   // a <= D <= K
 struct AcceptArgs {
   TreeDev t;
   PagedDev kv;
-  int layers, chunks;          // 16-byte columns per row
+  int chunks;                  // 16-byte columns per row
   long long layer_stride;      // columns per layer
   const int32_t* best_path;
   const int32_t* accept_len;
@@ -119,7 +119,6 @@ medusa_status_t launch_paged_accept(const TreeDev& t, const PagedDev& kv, int la
   AcceptArgs a{};
   a.t = t;
   a.kv = kv;
-  a.layers = layers;
   a.chunks = kv.hd * (dtype == MEDUSA_BF16 ? 2 : 4) / 16;
   a.layer_stride = (static_cast<long long>(kv.n_pages) * kv.Hkv << kv.page_shift) * a.chunks;
   a.best_path = best_path;

@@ -1,6 +1,8 @@
 // Attention of new tokens over a paged cache, fp32 arithmetic on the CUDA
-// cores: every dtype, head size and group size (the tensor-core kernel of
-// paged_attention_tc.cu takes bf16 heads of 64 and 128).
+// cores: every dtype, head size and group size.  Bf16 heads of 64 and 128
+// come here only with a scale of at most 0, or in groups of more than 128 query
+// heads; otherwise paged_attention_few.cu takes them where a sequence's rows of
+// a key head are few, paged_attention_tc.cu the rest.
 //
 // One pass over the keys with a running maximum and sum per query row: with
 // m' = max(m, max_j s_j), O <- O 2^(m - m') + sum_j 2^(s_j - m') V_j and the
@@ -8,14 +10,15 @@
 // A CTA holds R query rows and takes 32 or 64 keys at a time through shared
 // memory as fp32; a thread owns R / 16 or R / 8 rows x 2 or 4 keys of the
 // scores and the same rows x HD / 16 dimensions of O, so one 16-byte
-// shared-memory read feeds 8 to 16 products.  The probabilities take the place
-// of the keys, which leaves room for more CTAs per SM: some compute while the
-// others' loads are in flight.
+// shared-memory read feeds 4 products of the scores and 5 to 7 of the outputs
+// (R = 16), or 8 and 8 to 13 (R = 64).  The probabilities take the place of the
+// keys, which leaves room for more CTAs per SM: some compute while the others'
+// loads are in flight.
 //
 // R = 16 where a sequence's rows fit (decoding and small trees): bound by the
 // latency of a block's loads, products and barriers, hence blocks of 32 keys,
 // four or five CTAs per SM, and warps without a row that only load (4 tokens
-// of 32 fp32 heads over 2721 rows 108 us, 3.3 TB/s; blocks of 64 keys, two
+// of 32 fp32 heads over 2721 rows 103 us, 3.5 TB/s; blocks of 64 keys, two
 // CTAs and every warp computing took 263).  R = 64 otherwise, bound by fp32
 // arithmetic and its shared-memory reads (4 x 257 tokens of the same heads
 // 1.78 ms, 27 TFLOP/s).
@@ -408,8 +411,12 @@ medusa_status_t launch_paged_attention(const PagedDev& kv, medusa_dtype_t dtype,
   w.by_g = Divisor(w.g);
   w.by_R = Divisor(w.R);
   w.by_hk = Divisor(kv.Hkv);
+  // Both measured: a 15-node fp32 tree of 4 heads over 4000 rows 23.5 us (no bound on the cut: 36.1, 0.15: 23.7), 64
+  // tokens of 4 heads on one after 1500 rows 30.9 (31.1, with 0.1 36.8).  Extra blocks behind a unit only cost: 29
+  // ragged fp32 tokens of 40 heads on 8 over 50..700 rows 42.0 us (one: 43.9, two: 45.7), 257 tokens of 64 heads 63.1
+  // (one: 68.0).
   w.join = c.R == 16 ? 0.03f : 0.02f;
-  w.extra = c.R == 16 ? 1u : 0u;
+  w.extra = 0u;
   w.slots = static_cast<float*>(ws);
   w.counters = counters_of(ws);
   const int grid = sm_count() * c.per_sm;

@@ -136,6 +136,7 @@ struct Cut {
   }
   static __device__ __forceinline__ int tiles_of(const Work& w, int n) { return (n * w.g + w.R - 1) / w.by_R; }
 
+  static_assert(MEDUSA_MAX_B <= 64, "two sequences to a lane of the plan's warp");
   // One whole warp; the other threads see the plan after the next __syncthreads.
   static __device__ void plan(const Work& w, Plan& p) {
     const int lane = threadIdx.x & 31, B = w.kv.B;
@@ -239,6 +240,7 @@ struct Cut {
           p.b = 2 * lane + i;
           p.h = static_cast<int>(h);
           p.tile = static_cast<int>(u - h * nt);
+          // Inside 32 bits: the condition above holds only for W <= 2 C (C - units) / units, so nb k <= 2 C^3 < 2^30.
           p.block = static_cast<int>(nb * part / k);
           p.end = nb * (part + 1) / k - p.block;
           p.lo = static_cast<int>(at + u * k);

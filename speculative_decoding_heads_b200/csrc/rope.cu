@@ -19,7 +19,6 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTok = 32;     // tokens per block
-constexpr int kBatch = 1;       // tokens a thread loads before it stores any
 
 struct RopeArgs {
   PagedDev kv;
@@ -154,11 +153,11 @@ __device__ int prepare_tokens(const RopeArgs& a, int n0, Place* place, float2* c
 }
 
 // 16-byte path: a thread owns vector j of one head (in the half layout also
-// its partner rot/2 further on) and walks the block's tokens, kBatch of them
-// with all loads in flight, so that addresses advance by constant strides and
-// a head's kind is decided once.  Narrow models put several tokens side by
-// side, wide ones sweep over their heads (one sweep per blockIdx.y when there
-// are few tokens).
+// its partner rot/2 further on) and walks the block's tokens; the next step's
+// loads are in flight while a step is turned and stored (two steps' registers
+// take turns; under the six blocks' 40 registers the compiler spills 52 bytes
+// of them in bf16).  Narrow models put several tokens side by side, wide ones
+// sweep over their heads (one sweep per blockIdx.y when there are few tokens).
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 6) rope_append_vec(const RopeArgs a) {
   constexpr int E = Vec16<T>::kE;
@@ -175,27 +174,23 @@ __global__ void __launch_bounds__(kThreads, 6) rope_append_vec(const RopeArgs a)
   const bool idle = i0 >= per || t0 >= side;
   const bool two = a.half && j < turned;
   const int va = j < turned ? j * E : a.rot + (j - turned) * E;   // element offset of the (first) vector
-  struct Step {                                               // kBatch tokens of one head
-    int h, tb, kind, hk;                                      // q, k or v, and the head in it
-    uint4 x[kBatch], y[kBatch];
+  struct Step {                                               // a token of one head
+    int h, t, kind, hk;                                       // q, k or v, and the head in it
+    uint4 x, y;
   };
   auto load = [&](Step& s) {
     s.kind = s.h < H ? 0 : s.h < H + Hkv ? 1 : 2;
     s.hk = s.kind == 0 ? s.h : s.kind == 1 ? s.h - H : s.h - H - Hkv;
     const long long step = s.kind == 0 ? a.qs : s.kind == 1 ? a.ks : a.vs;
-    const T* src = static_cast<const T*>(s.kind == 0 ? a.q : s.kind == 1 ? a.k : a.v) + (n0 + s.tb) * step + s.hk * hd + va;
-#pragma unroll
-    for (int m = 0; m < kBatch; ++m) {
-      if (s.tb + m * side >= count) continue;
-      s.x[m] = *reinterpret_cast<const uint4*>(src + m * side * step);
-      if (two) s.y[m] = *reinterpret_cast<const uint4*>(src + m * side * step + pairs);
-    }
+    const T* src = static_cast<const T*>(s.kind == 0 ? a.q : s.kind == 1 ? a.k : a.v) + (n0 + s.t) * step + s.hk * hd + va;
+    s.x = *reinterpret_cast<const uint4*>(src);
+    if (two) s.y = *reinterpret_cast<const uint4*>(src + pairs);
   };
   auto follow = [&](const Step& s, Step& next) {              // false: s was the last
     next.h = s.h;
-    next.tb = s.tb + kBatch * side;
-    if (next.tb >= count) {
-      next.tb = t0;
+    next.t = s.t + side;
+    if (next.t >= count) {
+      next.t = t0;
       next.h += gridDim.y * per;
     }
     return next.h < heads;
@@ -203,46 +198,42 @@ __global__ void __launch_bounds__(kThreads, 6) rope_append_vec(const RopeArgs a)
   auto finish = [&](Step& s) {
     T* dst = s.kind == 0 ? static_cast<T*>(a.q_out) + (static_cast<long long>(n0) * H + s.hk) * hd + va
                          : static_cast<T*>(s.kind == 1 ? a.kv.k : a.kv.v) + (static_cast<long long>(s.hk) * hd << a.kv.page_shift) + va;
+    if (place[s.t].base < 0) return;
+    if (j < turned && s.kind < 2) {
+      const float2* w = cs + s.t * pairs + (a.half ? va : va >> 1);
+      float f[E];
+      Vec16<T>::unpack(s.x, f);
+      if (two) {
+        float g[E];
+        Vec16<T>::unpack(s.y, g);
 #pragma unroll
-    for (int m = 0; m < kBatch; ++m) {
-      const int t = s.tb + m * side;
-      if (t >= count || place[t].base < 0) continue;
-      if (j < turned && s.kind < 2) {
-        const float2* w = cs + t * pairs + (a.half ? va : va >> 1);
-        float f[E];
-        Vec16<T>::unpack(s.x[m], f);
-        if (two) {
-          float g[E];
-          Vec16<T>::unpack(s.y[m], g);
-#pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float p = f[e] * w[e].x - g[e] * w[e].y, r = g[e] * w[e].x + f[e] * w[e].y;
-            f[e] = p;
-            g[e] = r;
-          }
-          s.y[m] = Vec16<T>::pack(g);
-        } else {
-#pragma unroll
-          for (int e = 0; e < E / 2; ++e) {
-            const float p = f[2 * e] * w[e].x - f[2 * e + 1] * w[e].y, r = f[2 * e + 1] * w[e].x + f[2 * e] * w[e].y;
-            f[2 * e] = p;
-            f[2 * e + 1] = r;
-          }
+        for (int e = 0; e < E; ++e) {
+          const float p = f[e] * w[e].x - g[e] * w[e].y, r = g[e] * w[e].x + f[e] * w[e].y;
+          f[e] = p;
+          g[e] = r;
         }
-        s.x[m] = Vec16<T>::pack(f);
+        s.y = Vec16<T>::pack(g);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E / 2; ++e) {
+          const float p = f[2 * e] * w[e].x - f[2 * e + 1] * w[e].y, r = f[2 * e + 1] * w[e].x + f[2 * e] * w[e].y;
+          f[2 * e] = p;
+          f[2 * e + 1] = r;
+        }
       }
-      T* to = dst + (s.kind == 0 ? static_cast<long long>(t) * H * hd : place[t].base);
-      *reinterpret_cast<uint4*>(to) = s.x[m];
-      if (two) *reinterpret_cast<uint4*>(to + pairs) = s.y[m];
+      s.x = Vec16<T>::pack(f);
     }
+    T* to = dst + (s.kind == 0 ? static_cast<long long>(s.t) * H * hd : place[s.t].base);
+    *reinterpret_cast<uint4*>(to) = s.x;
+    if (two) *reinterpret_cast<uint4*>(to + pairs) = s.y;
   };
   // The first loads wait for nothing: they run while the places and angles are
   // worked out; later ones run while the step before is turned and stored
   // (every vector is read before it is written, also when q_out is q).
   Step s0, s1;
   s0.h = i0 - t0 * heads + blockIdx.y * per;
-  s0.tb = t0;
-  const bool some = !idle && s0.h < heads && s0.tb < count;
+  s0.t = t0;
+  const bool some = !idle && s0.h < heads && s0.t < count;
   if (some) load(s0);
   prepare_tokens<T>(a, n0, place, cs);
   if (!some) return;
@@ -331,6 +322,9 @@ medusa_status_t launch_rope_append(const PagedDev& kv, medusa_dtype_t dtype, int
   const int E = 16 / es;
   const bool vec = (a.half ? a.rot / 2 : a.rot) % E == 0;
   const int turned = a.half ? a.rot / 2 / E : a.rot / E, per = vec ? kThreads / (turned + (kv.hd - a.rot) / E) : 1;
+  // Up to two tokens per SM: a block of its own for every sweep over the heads (one token of 64 + 2 x 8 heads
+  // 3.6 us, one block 4.9; 64 of 32 + 2 x 32 4.0, 5.1).  With more, every block would set up its tokens again for
+  // each (400 of 32 + 2 x 32 6.7 us, with them 7.1).
   const int sweeps = N <= 2 * sm_count() ? (H + 2 * kv.Hkv + per - 1) / per : 1;
   if (dtype == MEDUSA_BF16) {
     if (vec) rope_append_vec<uint16_t><<<dim3(grid, sweeps), kThreads, smem, stream>>>(a);
