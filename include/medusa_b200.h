@@ -602,10 +602,15 @@ size_t medusa_paged_attention_workspace_size(const medusa_paged_kv_t* kv, int N,
  *               chunk_starts must be NULL
  *   q, out [N, H, hd] contiguous in the cache's dtype, H a multiple of Hkv;
  *              out apart from q and from the pages.
- * fp32 scores, softmax and accumulation; in bf16 the probabilities enter the
- * second product rounded to bf16 and the output is rounded once.  |scale| is
- * at most 2^64.  Results do not depend on the order in which the GPU runs the
- * blocks.  A non-finite value row of a NEW token can reach the other new rows
+ * fp32 scores, softmax and accumulation; a bf16 output is rounded once.  In
+ * bf16 (hd 64 and 128, scale > 0) the probabilities enter the second product as
+ * a bf16 pair, without an error of their own, in calls with few rows (at most
+ * 16, or 4 for hd 128 with more units of a sequence and key head than four per
+ * SM; a row is a token and a query head of the group, and with chunk_starts all
+ * N tokens count as one sequence's), and rounded to bf16 in all others, which
+ * adds an error as large as the output's rounding: a request's row can differ
+ * by that much between batches.  |scale| is at most 2^64.  Results do not
+ * depend on the order in which the GPU runs the blocks.  A non-finite value row of a NEW token can reach the other new rows
  * of its sequence (its weight there is zero, and 0 * inf is NaN). */
 medusa_status_t medusa_paged_attention(const medusa_paged_kv_t* kv, int layer, int N, int H, const void* q,
                                        float scale, const medusa_tree_t* tree, const int32_t* chunk_starts,
@@ -658,6 +663,8 @@ typedef struct medusa_logit_rules {
  *   z = z + the sum of bias over the entries with bias_ids = v (in list order)
  *   z = -inf where allowed has v's bit clear (a node whose mask is empty gets
  *       a row of -inf)
+ * in fp32, as one multiply-add: z m + c with m = 1, repetition or its rounded
+ * reciprocal, and c = bias - penalties, each rounded once.
  * A tree of the root alone (T = 1) is the form for single tokens.  Tokens
  * outside [0, V) are skipped (padding).  history_lens[b] outside [0,
  * history_cap] or prompt_lens[b] < 0 sets MEDUSA_ERR_DEVICE_CHECK and leaves

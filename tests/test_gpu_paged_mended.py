@@ -1,10 +1,12 @@
 """The paged-cache calls on the GPU where arguments or the machine let them down."""
 
+import numpy as np
 import pytest
 import torch
 
 import oracle.medusa_oracle as O
-from test_gpu_paged import Cache, ints
+import oracle.paged_oracle as PO
+from test_gpu_paged import Cache, f64, ints, starts_of
 
 pytestmark = pytest.mark.gpu
 
@@ -117,3 +119,54 @@ def test_the_most_rows_of_a_sequence(mb):
     mb.medusa_paged_attention(kv, 0, x[:2].contiguous(), out, 1.0, ws)
     assert mb.device_status() == (mb.MEDUSA_ERR_DEVICE_CHECK, 11)
     assert out[0].isfinite().all() and not (out[0] == 7).any() and (out[1] == 7).all()
+
+
+ERRORS = [
+    # hd, page, H, Hkv, lens, news (None: a tree of so many nodes), nodes, probabilities as a pair
+    (128, 16, 8, 8, [700, 1100, 33], [1, 1, 1], 0, True),
+    (64, 16, 8, 2, [700], [4], 0, True),
+    (128, 64, 4, 4, [300, 77], None, 64, False),              # alternating tiles
+    (64, 16, 8, 2, [200], None, 48, False),
+    (128, 16, 4, 4, [127, 500], [130, 3], 0, False),          # ragged chunks, one group of rows
+    (128, 64, 64, 8, [300, 40], [400, 140], 0, False),        # two groups of rows
+    (64, 32, 64, 8, [0, 130], [303, 300], 0, False),
+    (128, 16, 8, 8, [400, 9, 33], [1, 1, 20], 0, False),      # single tokens that travel with a prompt
+]
+
+
+@pytest.mark.parametrize("case", ERRORS, ids=lambda c: "-".join(str(x) for x in c))
+def test_the_error_of_bf16_attention(mb, case):
+    """Root mean square against 64 bits: the output's one rounding and, where the probabilities are one bf16 each, theirs.
+    A rounding to bf16 is off by at most 2^-8 of the value, evenly spread and so 2^-8 / sqrt(3) in root mean square; those
+    of different keys are independent, so their squares add up: (2^-8)^2 / 3 times the sum over the keys of (p v)^2.  A
+    pair leaves half a step of a remainder that is itself half a step, 2^-16; scores, exponentials and sums in fp32 stay
+    below 2^-13 for these up to 1100 keys.  Beside the output's rounding of over 2^-10 that is less than 1% in squares,
+    and 5% leaves room for values that round the other way."""
+    hd, page, H, Hkv, lens, news, nodes, as_pair = case
+    tree = sees = None
+    if news is None:
+        tree = mb.Tree(O.ranksum_choices(5, 10, nodes), 5, 10)
+        anc = tree.tables()["anc"]
+        sees = np.array([[(anc[i][j // 64] >> (j % 64)) & 1 for j in range(tree.T)] for i in range(tree.T)], bool)
+    count = [tree.T] * len(lens) if news is None else news
+    starts = starts_of(count)
+    c = Cache(mb, "bf16", hd, page, Hkv, lens, count, seed=nodes)
+    q = c.randn(sum(count), H, hd).bfloat16().cuda()
+    out = torch.full_like(q, 7.0)
+    ws = mb.workspace(mb.medusa_paged_attention_workspace_size(c.kv, q.shape[0], H))
+    mb.medusa_paged_attention(c.kv, 0, q, out, hd ** -0.5, ws, tree=tree,
+                              chunk_starts=None if len(set(count)) == 1 else ints(starts))
+    k, v, q = f64(c.k[0]), f64(c.v[0]), f64(q)
+    want, _ = PO.attention(q, k, v, c.table, lens, starts, hd ** -0.5, sees)
+    once = np.mean((f64(torch.from_numpy(want).bfloat16()) - want) ** 2)
+    theirs = np.zeros_like(want)
+    for b, (L, n) in enumerate(zip(lens, count)):
+        kb, vb = (np.repeat(PO.gather_rows(x, c.table[b], L + n), H // Hkv, 0) for x in (k, v))
+        qb = q[starts[b]:starts[b + 1]].transpose(1, 0, 2)
+        visible = np.concatenate([np.ones((n, L), bool), sees if sees is not None else np.tril(np.ones((n, n), bool))], 1)
+        p = np.exp(np.where(visible, qb @ kb.transpose(0, 2, 1) * hd ** -0.5, -np.inf))
+        p /= p.sum(-1, keepdims=True)
+        theirs[starts[b]:starts[b + 1]] = (p ** 2 @ vb ** 2).transpose(1, 0, 2)
+    assert once > 2.0 ** -20 * np.mean(want ** 2)
+    most = once + (0 if as_pair else np.mean(theirs) * 2.0 ** -16 / 3)
+    assert np.mean((f64(out) - want) ** 2) < 1.05 ** 2 * most
