@@ -36,13 +36,15 @@
 // through one ring in the order in which they are used.  Every wait is bounded.
 //
 // Measured: chunks of 3001 and 4096 tokens of 32 heads (8 key heads) after
-// 2048..4095 rows 480-550 us, 1000-1150 TFLOP/s (a tile is 1024 clocks of
-// products and about 2300 of softmax latency, so two groups leave the tensor
-// cores a third of the time; without the exponentials it takes 6% less, with
-// half of the products 11%).  Four 65-node trees of 52 heads over 8192 rows
-// 150-155 us, 5.8 TB/s.  Halves of 64 keys with double-buffered scores (620
-// us), two threads per row (1055) and polynomials for a share of the
-// exponentials (526-575) were slower.
+// 2048..4095 rows 473 us in short bursts at 1.965 GHz, 1160 TFLOP/s, and 551 us
+// in calls without end, which the power cap holds at 1.67 GHz (as many clocks).
+// A tile is 1024 clocks of products and about 2300 of softmax latency, so two
+// groups leave the tensor cores a third of the time; the exponentials alone are
+// not it (without them 2048 tokens after 2048 rows take 109 us, 111 with).
+// Four 65-node trees of 52 heads over 8192 rows 150 us in bursts, 5.8 TB/s, and
+// 165-176 at the cap's 1.25 GHz.  Halves of 64 keys with double-buffered scores
+// (620 us where this took 518), two threads per row (1055) and polynomials for
+// a share of the exponentials (526-575) were slower.
 #include <cudaTypedefs.h>
 
 #include "paged_work.cuh"
