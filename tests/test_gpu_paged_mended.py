@@ -6,7 +6,7 @@ import torch
 
 import oracle.medusa_oracle as O
 import oracle.paged_oracle as PO
-from test_gpu_paged import Cache, f64, ints, starts_of
+from test_gpu_paged import Cache, check_attention, f64, ints, starts_of
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,78 @@ def test_the_error_of_bf16_attention(mb, case):
     assert once > 2.0 ** -20 * np.mean(want ** 2)
     most = once + (0 if as_pair else np.mean(theirs) * 2.0 ** -16 / 3)
     assert np.mean((f64(out) - want) ** 2) < 1.05 ** 2 * most
+
+
+# ---------------------------------------------------------------------------
+# calls that the documentation allows, at the ends of their ranges
+# ---------------------------------------------------------------------------
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 128), ("bf16", 64), ("bf16", 40), ("f32", 64)])
+@pytest.mark.parametrize("news,rows", [([0, 0, 0], 4), ([0, 0, 0], 40), ([2, 0, 1], 5), ([30, 0, 11], 60)], ids=str)
+def test_rows_behind_the_last_chunk_stay(mb, dtype, hd, news, rows):
+    """More packed rows than chunks, and chunks that are all empty, by every kernel: those rows keep what they held."""
+    c = Cache(mb, dtype, hd, 16, 2, [20, 300, 5], news)
+    q = c.randn(rows, 4, hd).to(c.k.dtype).cuda()
+    starts = starts_of(news)
+    ws = mb.workspace(mb.medusa_paged_attention_workspace_size(c.kv, rows, 4))
+    out = torch.full_like(q, 7.0)
+    for _ in range(2):
+        mb.medusa_paged_attention(c.kv, 0, q, out, 0.1, ws, chunk_starts=ints(starts))
+        assert (out[starts[-1]:] == 7).all()
+    if starts[-1]:
+        want, mass = PO.attention(f64(q[:starts[-1]]), f64(c.k[0]), f64(c.v[0]), c.table, [20, 300, 5], starts, 0.1)
+        # probabilities and output rounded to bf16 (2^-8 each); fp32 terms far below 2^-10 for these scores
+        tol = mass * (2.0 ** -8 + 2.0 ** -10) + np.abs(want) * 2.0 ** -8 if dtype == "bf16" else mass * 2.0 ** -10
+        assert (np.abs(f64(out[:starts[-1]]) - want) <= tol).all()
+
+
+@pytest.mark.parametrize("case", [
+    ("f32", 64, 16, 4, 1, [40, 3, 0, 9, 100, 7, 7, 7], [8, 0, 0, 0, 0, 0, 0, 0]),     # 32 rows where the average is 4: two tiles of 16
+    ("bf16", 40, 16, 4, 1, [40, 3, 0, 9, 100, 7, 7, 7], [0, 1, 0, 7, 0, 0, 0, 0]),
+    ("bf16", 128, 16, 20, 10, [3 * b for b in range(64)], [1] * 64),                  # 640 units: few rows, and more than four
+    ("bf16", 128, 16, 20, 10, [3 * b for b in range(64)], [3] * 64),
+    ("bf16", 64, 16, 20, 10, [3 * b for b in range(64)], [3] * 64),
+], ids=["f32-tiles", "bf16-tiles", "many-units", "many-units-6-rows", "many-units-64"])
+def test_attention_at_the_bounds_between_the_kernels(mb, case):
+    check_attention(mb, *case)
+
+
+def test_too_many_blocks_of_keys(mb):
+    """Over 2^30 blocks of keys in a call: refused, with nothing computed."""
+    hd, page, Hkv = 8, 256, 40
+    pages = torch.zeros(1, 1, Hkv, page, hd, device="cuda")
+    table = torch.zeros(1, MOST_ROWS // page + 1, dtype=torch.int32, device="cuda")
+    kv = mb.PagedKV(pages, pages.clone(), table, ints([MOST_ROWS - 1]))
+    assert (MOST_ROWS // 32) * Hkv > 2 ** 30
+    q = torch.zeros(1, Hkv, hd, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ws = mb.workspace(mb.medusa_paged_attention_workspace_size(kv, 1, Hkv))
+    mb.medusa_paged_attention(kv, 0, q, out, 1.0, ws)
+    assert mb.device_status() == (mb.MEDUSA_ERR_DEVICE_CHECK, 11)
+    assert (out == 7).all() and not ws.any()
+
+
+@pytest.mark.parametrize("dtype,hd", [("bf16", 64), ("f32", 8)])
+def test_a_prefix_of_millions_of_rows(mb, dtype, hd):
+    """A prefix whose pages are all the same page: every row has the weight of its copies, so the output is that of the
+    one page, the new token aside.  Scores are zero, which makes the weights equal: the mean of the values."""
+    page, L = 256, 3_000_000 * 2 - 1
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.randn(1, 2, 1, page, hd, generator=g, device="cuda").to(t)
+    v = (torch.randn(1, 2, 1, page, hd, generator=g, device="cuda") + 1).to(t)
+    table = torch.zeros(1, L // page + 1, dtype=torch.int32, device="cuda")
+    table[0, -1] = 1
+    kv = mb.PagedKV(k, v, table, ints([L]))
+    q = torch.zeros(1, 4, hd, dtype=t, device="cuda")
+    out = torch.full_like(q, 7.0)
+    ws = mb.workspace(mb.medusa_paged_attention_workspace_size(kv, 1, 4))
+    mb.medusa_paged_attention(kv, 0, q, out, 1.0, ws)
+    copies, last = (L + 1) // page, (L + 1) % page
+    want = (f64(v[0, 0, 0]).sum(0) * copies + f64(v[0, 1, 0, :last]).sum(0)) / (L + 1)
+    # A block's range is at most 6 million / 148 rows, below 2^16, and at most 2^10 ranges are joined: a sum of n terms is
+    # off by n 2^-24 of their absolute sum at the very most, twice (numerator and denominator); then the output's rounding.
+    mass = (np.abs(f64(v[0, 0, 0])).sum(0) * copies + np.abs(f64(v[0, 1, 0, :last])).sum(0)) / (L + 1)
+    tol = mass * 2 * (2.0 ** -8 + 2.0 ** -14) + (np.abs(want) * 2.0 ** -8 if dtype == "bf16" else 0)
+    assert (np.abs(f64(out[0]) - want) <= tol).all()
